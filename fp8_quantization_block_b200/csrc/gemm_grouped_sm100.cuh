@@ -1,0 +1,282 @@
+// gemm_grouped_sm100.cuh -- block-scaled GEMM of rows grouped by expert.
+//
+// For each group g, C[rows of g] = A_dq[rows of g] * (B_g)_dq^T, every B_g an
+// [N x K] matrix of its own.  The single-CTA kernel of gemm_sm100.cuh (its
+// roles, rings, TMEM plan and epilogue) on tiles that the device finds itself:
+// group sizes are device data, so each warp role walks the groups (groups.cuh)
+// in step with the others.  A's scales begin a 128-row band per group
+// (quantize_grouped_kernel), so a 128-row tile reads one whole band; a tile's
+// rows past the group's end are the next group's or past the matrix, and only
+// produce accumulator rows that are not stored.  Tiles of a group run rows
+// fastest: neighbouring CTAs share a 256-row slice of B_g.
+#pragma once
+
+#include "gemm_sm100.cuh"
+#include "groups.cuh"
+
+namespace mx {
+
+template <int FMT, int STAGES>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmSfa,
+                        const __grid_constant__ CUtensorMap tmSfb, GemmParams p, const Groups groups) {
+    constexpr int BN = 256;
+    using F = GemmFmt<FMT>;
+    using L = GemmSmem<FMT, BN, STAGES>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+    uint64_t *empty = full + STAGES;
+    uint64_t *sfload = empty + STAGES;           // [kSfGroups]
+    uint64_t *sfree = sfload + L::kSfGroups;     // [kSfGroups]
+    uint64_t *acc_full = sfree + L::kSfGroups;   // [2]
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *mma_done = acc_empty + 1;
+    uint64_t *sf_full = mma_done + 1;            // [L::kSlots]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 4);
+    uint32_t *ready_count = reinterpret_cast<uint32_t *>(smem + L::kOffMisc + 8);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int worker = (int)blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int g = 0; g < L::kSfGroups; ++g) {
+            mbar_init(&sfload[g], 1);
+            mbar_init(&sfree[g], 4);
+        }
+        mbar_init(&acc_full[0], 1);
+        mbar_init(&acc_full[1], 1);
+        mbar_init(acc_empty, (p.epilogue == 1 ? 2 : 1) * kEpiWarps);
+        mbar_init(mma_done, 1);
+        for (int i = 0; i < L::kSlots; ++i) mbar_init(&sf_full[i], 4);
+        *abort_flag = 0;
+        *ready_count = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSfa);
+        tma_prefetch_desc(&tmSfb);
+        if (p.use_tma_store) tma_prefetch_desc(&tmC);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, L::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();   // the operands and the offsets may be the previous kernel's
+
+    // the work units of this CTA: tiles worker, worker + grid, ...
+    p.ks.tiles = GroupWalk::count_blocks(groups, 7, lane) * p.n_blocks;
+    p.ks.workers = (int)gridDim.x;
+    const int n_units = unit_count<false>(p, worker);
+    GroupWalk walk(groups, 7, lane);
+    struct Tile {
+        int group, row0, row_end, n0, a_band;
+    };
+    auto tile_at = [&](int u) {   // u ascending within a warp
+        GroupBlock b;
+        Tile t{0, 0, 0, 0, 0};
+        const int i = worker + u * p.ks.workers;
+        if (walk.find(i / p.n_blocks, b)) {
+            const int local = i - b.first * p.n_blocks, nb = local / b.blocks, mb = local - nb * b.blocks;
+            t = Tile{b.group, b.start + mb * kBM, b.end, nb * BN, b.first + mb};
+        }
+        return t;
+    };
+    const int b_bands = (p.N + 127) / 128;   // scale bands of one B_g
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ code-tile producer
+        if (!p.skip_producer) {
+            int used = 0, s = 0;
+            uint32_t ph = 0;
+            bool stop = false;
+            for (int u = 0; u < n_units && !stop; ++u) {
+                const Tile t = tile_at(u);
+                for (int kt = 0; kt < p.num_kt; ++kt) {
+                    if (!mbar_wait_bounded(&empty[s], ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
+                        stop = true;
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&full[s], FMT == kGemmRuntimeTypes ? p.stage_tx
+                                                                                 : (uint32_t)(L::kABytes + L::kBBytes));
+                        tma_load_2d(smem + L::kOffA + s * L::kABytes, &tmA, kt * kStageKBytes, t.row0, &full[s]);
+                        tma_load_2d(smem + L::kOffB + s * L::kBBytes, &tmB, kt * kStageKBytes, t.group * p.N + t.n0,
+                                    &full[s]);
+                    }
+                    __syncwarp();
+                    ++used;
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            for (int u = max(0, used - STAGES); u < used; ++u)
+                mbar_wait_bounded(&full[u % STAGES], (uint32_t)((u / STAGES) & 1), p.wait_limit_ns, SITE_GEMM_TAIL,
+                                  nullptr);
+        }
+    } else if (warp == kSfWarp) {
+        // ------------------------------------------------------------ scale-tile producer
+        if (!p.skip_producer) {
+            int u = 0;   // the role asks for this worker's tiles in order
+            sf_producer_role<L, false>(p, &tmSfa, &tmSfb, smem, sfload, sfree, worker,
+                                       [&](int, int &a_band, int &b_band) {
+                                           const Tile t = tile_at(u++);
+                                           a_band = t.a_band;
+                                           b_band = t.group * b_bands + t.n0 / 128;
+                                       },
+                                       lane, abort_flag);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint64_t desc_ab = smem_desc(0, 16, 1024, 2);
+        const uint64_t ad0 = desc_ab | (uint64_t)((smem_u32(smem + L::kOffA) >> 4) & 0x3FFFu);
+        const uint64_t bd0 = desc_ab | (uint64_t)((smem_u32(smem + L::kOffB) >> 4) & 0x3FFFu);
+        const uint32_t leader = lane == 0 ? 1u : 0u;
+        const uint32_t ab = FMT == kGemmRuntimeTypes ? p.ab_types : 0u;
+        int last_n_mma, last_n_chunk;
+        stage_extent<FMT>(p.num_kt - 1, p.K, last_n_mma, last_n_chunk);
+        int s = 0, slot = 0;
+        uint32_t kg = 0, avail = 0;
+        bool stop = false;
+        for (int it = 0; it < n_units && !stop; ++it) {
+            const uint32_t t_acc = tmem + (uint32_t)((it & 1) * L::kAccStride);
+            auto run_stage = [&](int k, uint32_t acc) {
+                const uint32_t t_sfa = tmem + (uint32_t)(L::kTmemSf + slot * L::kSfSlotCols);
+                issue_stage<FMT, false, BN, 4 * L::kBBands>(
+                    k + 1 < p.num_kt ? 4 : last_n_mma, t_acc, ad0 + (uint64_t)(s * (L::kABytes >> 4)),
+                    bd0 + (uint64_t)(s * (L::kBBytes >> 4)), t_sfa, t_sfa + 4 * F::kChunks, acc, leader, ab);
+                tc_commit_if(&empty[s], leader);
+                s = (s + 1 == STAGES) ? 0 : s + 1;
+                slot = (slot + 1 == L::kSlots) ? 0 : slot + 1;
+                ++kg;
+            };
+            for (int kt = 0; kt < p.num_kt; kt += 2) {
+                const bool two = kt + 1 < p.num_kt;
+                const uint32_t need = kg + (two ? 1u : 0u);
+                if (need >= avail) {
+                    avail = wait_counter_above(ready_count, need, p.wait_limit_ns, SITE_GEMM_MMA_READY, abort_flag);
+                    if (avail == 0u) {
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                if (kt == 0 && it > 0) {
+                    if (!mbar_wait_bounded(acc_empty, (it - 1) & 1, p.wait_limit_ns, SITE_GEMM_MMA_ACC_EMPTY, abort_flag)) {
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                run_stage(kt, kt > 0 ? 1u : 0u);
+                if (two) run_stage(kt + 1, 1u);
+            }
+            if (!stop) tc_commit_if(&acc_full[it & 1], leader);
+        }
+        tc_commit_if(mma_done, leader);
+        __syncwarp();
+    } else if (warp == kGateWarp) {
+        // ------------------------------------------------------------ gate
+        gate_role<STAGES, L::kSlots>(p, full, sf_full, ready_count, n_units * p.num_kt, lane, abort_flag);
+    } else if (warp >= 6) {
+        // ------------------------------------------------------------ scale warps
+        const int q = warp & 3;
+        uint32_t amax = 0;
+        const float ga = FMT == 3 ? *p.ga : 1.0f;
+        // GELU: this warp's share of the shared accumulator columns of every
+        // tile but the last, as in gemm_kernel
+        int help_next = 0;
+        auto help = [&](int u) -> bool {
+            const Tile t = tile_at(u);
+            const int b = u & 1;
+            if (!mbar_wait_bounded(&acc_full[b], (u >> 1) & 1, p.wait_limit_ns, SITE_GEMM_EPI_ACC, abort_flag))
+                return false;
+            tc_fence_after();
+            p.M = t.row_end;
+            help_drain_t<BN, L::kAccStride, FMT == 3>(
+                p, tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * L::kAccStride), b, t.row0 + 32 * q, t.n0, lane,
+                amax, FMT == 3 ? ga * p.gb[t.group] : 1.0f);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty);
+            return true;
+        };
+        scale_role<L, STAGES, false>(p, smem, sfload, sfree, empty,
+                                     tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)L::kTmemSf, worker, lane, abort_flag,
+                                     [&](int slot) { mbar_arrive(&sf_full[slot]); },
+                                     [&](int kg) -> bool {
+                                         if (p.epilogue != 1) return true;
+                                         for (; help_next < n_units - 1 && kg - L::kSlots >= (help_next + 1) * p.num_kt;
+                                              ++help_next)
+                                             if (!help(help_next)) return false;
+                                         return true;
+                                     });
+        if (p.epilogue == 1 && !*abort_flag)
+            for (; help_next < n_units - 1; ++help_next)
+                if (!help(help_next)) break;
+        // the upper half of the columns of this CTA's last tile
+        if (n_units > 0 && !*abort_flag) {
+            const int it = n_units - 1, b = it & 1;
+            const Tile t = tile_at(it);
+            if (mbar_wait_bounded(mma_done, 0, p.wait_limit_ns, SITE_GEMM_EPI_ACC, abort_flag)) {
+                tc_fence_after();
+                uint8_t *bufs = smem + L::kOffB + (warp - 6) * L::kEpiBufs * kEpiChunkBytes;
+                uint32_t nstore = 0;
+                p.M = t.row_end;
+                epilogue_chunks<L::kEpiBufs, FMT == 3, true>(
+                    p, &tmC, tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * L::kAccStride), t.row0 + 32 * q, t.n0,
+                    BN / 64, BN / 32, lane, bufs, nstore, amax, FMT == 3 ? ga * p.gb[t.group] : 1.0f);
+            }
+        }
+        epilogue_finish(p, lane, amax);
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;
+        uint8_t *bufs = smem + L::kOffEpi + (warp - 2) * L::kEpiBufs * kEpiChunkBytes;
+        uint32_t amax = 0, nstore = 0;
+        const float ga = FMT == 3 ? *p.ga : 1.0f;
+        for (int it = 0; it < n_units; ++it) {
+            const Tile t = tile_at(it);
+            const int b = it & 1;
+            if (!mbar_wait_bounded(&acc_full[b], (it >> 1) & 1, p.wait_limit_ns, SITE_GEMM_EPI_ACC, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t t_acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * L::kAccStride);
+            const float scale = FMT == 3 ? ga * p.gb[t.group] : 1.0f;
+            p.M = t.row_end;
+            if (it + 1 == n_units) {
+                // the last tile: the lower half of the columns
+                epilogue_chunks<L::kEpiBufs, FMT == 3, true>(p, &tmC, t_acc, t.row0 + 32 * q, t.n0, 0, BN / 64, lane,
+                                                             bufs, nstore, amax, scale);
+                break;
+            }
+            epilogue_tile<BN, L::kAccStride, L::kEpiBufs, FMT == 3, true>(p, &tmC, t_acc, b, t.row0 + 32 * q, t.n0, lane,
+                                                                         bufs, nstore, amax, scale, [&] {
+                                                                             if (lane == 0) mbar_arrive(acc_empty);
+                                                                         });
+        }
+        epilogue_finish(p, lane, amax);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        mbar_wait_bounded(mma_done, 0, p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
+        tmem_dealloc(tmem, L::kTmemCols);
+    }
+    griddep_launch_dependents();
+}
+
+}  // namespace mx

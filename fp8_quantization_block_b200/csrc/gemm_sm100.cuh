@@ -703,8 +703,10 @@ MX_DEVICE_INLINE void epi_load_convert(uint32_t t_addr, float scale, uint32_t (&
 // Write one converted chunk (rows m0q + lane, columns n0 + col ..) and fold
 // it into the running |C| maximum.  TMA stores go through NBUF staging
 // buffers of this warp, so a store only waits for the one issued NBUF
-// chunks earlier to have finished reading shared memory.
-template <int NBUF>
+// chunks earlier to have finished reading shared memory.  ROWS: p.M is the end
+// of a group's rows inside a larger C, which a TMA store would not clip at:
+// 32-row blocks across it are stored row by row.
+template <int NBUF, bool ROWS = false>
 MX_DEVICE_INLINE void epi_emit(const GemmParams &p, const CUtensorMap *tmC, const uint32_t (&packed)[16], int m0q,
                                int n0, int col, int lane, uint8_t *bufs, uint32_t &nstore, uint32_t &amax,
                                bool via_tma) {
@@ -726,6 +728,7 @@ MX_DEVICE_INLINE void epi_emit(const GemmParams &p, const CUtensorMap *tmC, cons
         }
     }
     if (m0q >= p.M) return;  // warp-uniform: no rows of this quadrant exist
+    if (ROWS && m0q + 32 > p.M) via_tma = false;
     if (via_tma) {
         uint8_t *buf = bufs + (nstore % NBUF) * kEpiChunkBytes;
         if (lane == 0) bulk_wait_group_read<NBUF - 1>();  // this buffer's previous store has read it
@@ -775,7 +778,7 @@ __host__ __device__ constexpr int gelu_help_chunks() {
 // GELU those chunks are pulled into registers first, so release() runs
 // before any store is issued and the tensor pipe idles only for the TMEM
 // reads.
-template <int BN, int ACC_STRIDE, int NBUF, bool SCALED, bool GELU, typename Release>
+template <int BN, int ACC_STRIDE, int NBUF, bool SCALED, bool GELU, bool ROWS, typename Release>
 MX_DEVICE_INLINE void epilogue_tile_t(const GemmParams &p, const CUtensorMap *tmC, uint32_t t_acc, int b, int m0q,
                                       int n0, int lane, uint8_t *bufs, uint32_t &nstore, uint32_t &amax, float scale,
                                       Release release) {
@@ -793,7 +796,7 @@ MX_DEVICE_INLINE void epilogue_tile_t(const GemmParams &p, const CUtensorMap *tm
             if (col >= n_valid) return;  // warp-uniform
             uint32_t packed[16];
             epi_load_convert<SCALED, GELU>(t_acc + (uint32_t)col, scale, packed);
-            epi_emit<NBUF>(p, tmC, packed, m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
+            epi_emit<NBUF, ROWS>(p, tmC, packed, m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
         };
         for (int idx = 0; idx < kMine; ++idx) drain(idx);
         tc_fence_before();
@@ -813,14 +816,14 @@ MX_DEVICE_INLINE void epilogue_tile_t(const GemmParams &p, const CUtensorMap *tm
 #pragma unroll
         for (int i = 0; i < kOv; ++i) {
             const int col = 32 * ((b == 0) ? (kChunks - kOv + i) : i);
-            if (col < n_valid) epi_emit<NBUF>(p, tmC, ov[i], m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
+            if (col < n_valid) epi_emit<NBUF, ROWS>(p, tmC, ov[i], m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
         }
         for (int i = 0; i < kChunks - kOv; ++i) {
             const int col = 32 * ((b == 0) ? i : (kOv + i));
             if (col >= n_valid) break;  // warp-uniform; columns ascend
             uint32_t packed[16];
             epi_load_convert<SCALED, GELU>(t_acc + (uint32_t)col, scale, packed);
-            epi_emit<NBUF>(p, tmC, packed, m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
+            epi_emit<NBUF, ROWS>(p, tmC, packed, m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
         }
     }
 }
@@ -829,7 +832,7 @@ MX_DEVICE_INLINE void epilogue_tile_t(const GemmParams &p, const CUtensorMap *tm
 // shared columns to release first): the last tile of a CTA, whose columns are
 // split between the epilogue warp and the scale warp of each TMEM lane
 // quadrant (the scale warps are idle once the tile's scales are in TMEM).
-template <int NBUF, bool SCALED, bool GELU>
+template <int NBUF, bool SCALED, bool GELU, bool ROWS>
 MX_DEVICE_INLINE void epilogue_chunks_t(const GemmParams &p, const CUtensorMap *tmC, uint32_t t_acc, int m0q, int n0,
                                         int c_begin, int c_end, int lane, uint8_t *bufs, uint32_t &nstore,
                                         uint32_t &amax, float scale) {
@@ -839,28 +842,28 @@ MX_DEVICE_INLINE void epilogue_chunks_t(const GemmParams &p, const CUtensorMap *
         if (col >= n_valid) break;  // warp-uniform; columns ascend
         uint32_t packed[16];
         epi_load_convert<SCALED, GELU>(t_acc + (uint32_t)col, scale, packed);
-        epi_emit<NBUF>(p, tmC, packed, m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
+        epi_emit<NBUF, ROWS>(p, tmC, packed, m0q, n0, col, lane, bufs, nstore, amax, p.use_tma_store);
     }
 }
-template <int NBUF, bool SCALED>
+template <int NBUF, bool SCALED, bool ROWS = false>
 MX_DEVICE_INLINE void epilogue_chunks(const GemmParams &p, const CUtensorMap *tmC, uint32_t t_acc, int m0q, int n0,
                                       int c_begin, int c_end, int lane, uint8_t *bufs, uint32_t &nstore,
                                       uint32_t &amax, float scale) {
     if (p.epilogue == 1)
-        epilogue_chunks_t<NBUF, SCALED, true>(p, tmC, t_acc, m0q, n0, c_begin, c_end, lane, bufs, nstore, amax, scale);
+        epilogue_chunks_t<NBUF, SCALED, true, ROWS>(p, tmC, t_acc, m0q, n0, c_begin, c_end, lane, bufs, nstore, amax, scale);
     else
-        epilogue_chunks_t<NBUF, SCALED, false>(p, tmC, t_acc, m0q, n0, c_begin, c_end, lane, bufs, nstore, amax, scale);
+        epilogue_chunks_t<NBUF, SCALED, false, ROWS>(p, tmC, t_acc, m0q, n0, c_begin, c_end, lane, bufs, nstore, amax, scale);
 }
 
-template <int BN, int ACC_STRIDE, int NBUF, bool SCALED, typename Release>
+template <int BN, int ACC_STRIDE, int NBUF, bool SCALED, bool ROWS = false, typename Release>
 MX_DEVICE_INLINE void epilogue_tile(const GemmParams &p, const CUtensorMap *tmC, uint32_t t_acc, int b, int m0q,
                                     int n0, int lane, uint8_t *bufs, uint32_t &nstore, uint32_t &amax, float scale,
                                     Release release) {
     if (p.epilogue == 1)
-        epilogue_tile_t<BN, ACC_STRIDE, NBUF, SCALED, true>(p, tmC, t_acc, b, m0q, n0, lane, bufs, nstore, amax, scale,
+        epilogue_tile_t<BN, ACC_STRIDE, NBUF, SCALED, true, ROWS>(p, tmC, t_acc, b, m0q, n0, lane, bufs, nstore, amax, scale,
                                                             release);
     else
-        epilogue_tile_t<BN, ACC_STRIDE, NBUF, SCALED, false>(p, tmC, t_acc, b, m0q, n0, lane, bufs, nstore, amax, scale,
+        epilogue_tile_t<BN, ACC_STRIDE, NBUF, SCALED, false, ROWS>(p, tmC, t_acc, b, m0q, n0, lane, bufs, nstore, amax, scale,
                                                              release);
 }
 

@@ -1,0 +1,104 @@
+// groups.cuh -- rows grouped by expert: walking the tiles of ragged groups.
+//
+// The rows [0, T) of a matrix belong to `count` groups one after another;
+// group g has the rows [offsets[g], offsets[g + 1]) (int32 in device memory,
+// so the host knows neither the sizes nor the number of tiles).  Each group is
+// cut into blocks of 2^shift rows of its own.  A warp finds the group of
+// block b among all groups' blocks by scanning 32 groups at a time, one per
+// lane: an inclusive prefix sum of their block counts by shuffles, then one
+// ballot.  Blocks are asked for in ascending order, so a walk loads each chunk
+// of 32 offsets once and the common step is the ballot alone; no table in
+// memory and no pass ahead of the kernel is needed.
+//
+// Offsets are clipped to [0, T], and a group that would end before it starts
+// is empty, so that no value of them makes a kernel read or write outside its
+// matrices.
+#pragma once
+
+#include "mx_common.cuh"
+
+namespace mx {
+
+struct Groups {
+    const int32_t *offsets;   // count + 1
+    int count;
+    int rows;                 // T
+};
+
+// One block: rows [row0, row1) hold the block's rows up to the group's end.
+struct GroupBlock {
+    int group;
+    int first;    // first block of the group among all groups' blocks
+    int blocks;   // blocks of the group
+    int start;    // the group's rows
+    int end;
+};
+
+class GroupWalk {
+  public:
+    // All lanes of the warp construct and call together.
+    MX_DEVICE_INLINE GroupWalk(const Groups &g, int shift, int lane) : g_(g), shift_(shift), lane_(lane) { load(0, 0); }
+
+    // The group that holds block `block` (ascending from call to call); false past the last one.
+    MX_DEVICE_INLINE bool find(int block, GroupBlock &out) {
+        while (block >= before_ + total_) {
+            if (base_ + 32 >= g_.count) return false;
+            load(base_ + 32, before_ + total_);
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, before_ + incl_ > block);
+        const int l = __ffs(m) - 1;   // m != 0: the chunk's last prefix exceeds block
+        out.group = base_ + l;
+        out.start = __shfl_sync(0xffffffffu, start_, l);
+        out.end = __shfl_sync(0xffffffffu, end_, l);
+        const int incl = __shfl_sync(0xffffffffu, incl_, l);
+        out.blocks = (out.end - out.start + (1 << shift_) - 1) >> shift_;
+        out.first = before_ + incl - out.blocks;
+        return true;
+    }
+
+    // Blocks of all groups together.
+    MX_DEVICE_INLINE static int count_blocks(const Groups &g, int shift, int lane) {
+        int n = 0;
+        for (int i = lane; i < g.count; i += 32) {
+            const int s = min(max(g.offsets[i], 0), g.rows), e = min(max(g.offsets[i + 1], 0), g.rows);
+            n += (max(e - s, 0) + (1 << shift) - 1) >> shift;
+        }
+        return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    }
+
+  private:
+    MX_DEVICE_INLINE void load(int base, int before) {
+        base_ = base;
+        before_ = before;
+        const int g = base + lane_;
+        int s = 0, e = 0;
+        if (g < g_.count) {
+            s = min(max(g_.offsets[g], 0), g_.rows);
+            e = max(min(max(g_.offsets[g + 1], 0), g_.rows), s);
+        }
+        start_ = s;
+        end_ = e;
+        int n = (e - s + (1 << shift_) - 1) >> shift_;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane_ >= o) n += v;
+        }
+        incl_ = n;
+        total_ = __shfl_sync(0xffffffffu, n, 31);
+    }
+
+    const Groups &g_;
+    int shift_, lane_;
+    int base_, before_, total_;     // the chunk's first group, the blocks before it and in it
+    int start_, end_, incl_;        // this lane's group, and the blocks up to its end
+};
+
+// 128-row bands of a grouped scale buffer: each group begins a band, so any
+// split of T rows into `count` groups fits in this many.
+__host__ __device__ inline int64_t group_bands(int64_t rows, int64_t count) {
+    const int64_t n = (rows + 127 * count) / 128;
+    return n < rows ? n : rows;
+}
+
+}  // namespace mx

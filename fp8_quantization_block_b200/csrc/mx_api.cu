@@ -1,7 +1,7 @@
 // mx_api.cu -- the C ABI of libmx.so (declared in include/mx.h): host-side
 // argument checks, TMA descriptor encoding and kernel launches.  The kernels
-// themselves live in quantize.cuh and gemm_sm100.cuh; this file is the single
-// translation unit of the library.
+// themselves live in quantize.cuh and gemm_sm100.cuh.  The block-128 FP8
+// formats and the experts' operators are mx_experts.cu's.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -15,6 +15,7 @@
 
 #include "mx.h"
 #include "mx_common.cuh"
+#include "mx_host.cuh"
 #include "quantize.cuh"
 #include "rotate.cuh"
 #include "gemm_sm100.cuh"
@@ -24,129 +25,6 @@
 namespace {
 
 using namespace mx;
-
-std::atomic<uint64_t> g_wait_limit_ns{1000000000ull};
-std::atomic<int> g_skip_producer{0};
-std::atomic<int> g_pair_enabled{1};
-std::atomic<int> g_pdl_enabled{1};
-std::atomic<int> g_max_gemm_ctas{0};  // 0: one CTA (or CTA pair) per SM pair of the device
-std::atomic<int> g_fused_mode{MX_FUSED_PIPELINED};  // how mx_gemm_fused_act runs (MX_DEBUG_FUSED_MODE)
-std::atomic<int> g_ksplit_mode{0};  // MX_DEBUG_K_SPLIT: 0 auto, 1 never, 2 whenever possible
-
-// Launch attributes shared by the kernels that may overlap the previous kernel
-// in the stream (they call griddep_wait() before reading any input).
-int pdl_attr(cudaLaunchAttribute *a) {
-    if (!g_pdl_enabled.load()) return 0;
-    a->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a->val.programmaticStreamSerializationAllowed = 1;
-    return 1;
-}
-
-bool valid_fmt(int fmt) { return fmt >= 0 && fmt <= 5; }
-int fmt_block(int fmt) { return (fmt == MX_NVFP4 || fmt == MX_MXFP4_MBS) ? 16 : 32; }
-int fmt_bits(int fmt) {
-    return (fmt == MX_MXFP4 || fmt == MX_NVFP4 || fmt == MX_MXFP4_MBS) ? 4 : (fmt == MX_MXFP6_E3M2 ? 6 : 8);
-}
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-// Blocking granularity a format needs along K (MXFP4-MBS: its 128-element macro blocks).
-int fmt_k_multiple(int fmt) { return fmt == MX_MXFP4_MBS ? 128 : fmt_block(fmt); }
-// Scale tiles, and for MXFP4-MBS the macro mantissas after them ([rows][cols/128], padded to 16).
-size_t tile_bytes(int fmt, int64_t rows, int64_t cols) {
-    return (size_t)(cdiv(rows, 128) * 128 * cdiv(cols / fmt_block(fmt), 4) * 4);
-}
-size_t scales_bytes(int fmt, int64_t rows, int64_t cols) {
-    size_t t = tile_bytes(fmt, rows, cols);
-    if (fmt == MX_MXFP4_MBS) t += (size_t)(cdiv(rows * (cols / 128), 16) * 16);
-    return t;
-}
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-mx_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MX_OK : MX_ERR_CUDA; }
-
-mx_status last_launch() {
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) {
-        fprintf(stderr, "libmx: launch failed: %s\n", cudaGetErrorString(e));
-        return MX_ERR_CUDA;
-    }
-    return MX_OK;
-}
-
-// --- cuTensorMapEncodeTiled through the runtime's driver entry point ---------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// 2D uint8 tensor [rows x row_bytes] (row pitch = row_bytes), box 128 bytes x box_rows, 128-byte swizzle.
-bool make_tmap_u8(CUtensorMap *m, const void *base, int64_t rows, int64_t row_bytes, int box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1u, 1u};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-// Codes of a kind::mxf8f6f4 operand as a 2D tensor of K elements per row, box
-// 128 elements x box_rows, 128-byte swizzle.  Every type lands in shared memory
-// as 128 bytes per row: FP8 bytes as they are; FP6 (16 codes in 12 bytes) and
-// FP4 (16 codes in 8 bytes) unpacked by the copy to one 16-byte group per 16
-// codes, the layout the MMA reads for these types.  The sub-byte types need a
-// 32-byte aligned base, row pitches that are multiples of 32 bytes and K a
-// multiple of 128 (the caller checks).
-bool make_tmap_codes_f8f6f4(CUtensorMap *m, int fmt, const void *base, int64_t rows, int64_t K, int box_rows) {
-    if (fmt_bits(fmt) == 8) return make_tmap_u8(m, base, rows, K, box_rows);
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const CUtensorMapDataType dt =
-        fmt_bits(fmt) == 6 ? CU_TENSOR_MAP_DATA_TYPE_16U6_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B;
-    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(K * fmt_bits(fmt) / 8)};
-    cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1u, 1u};
-    CUresult r = fn(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) fprintf(stderr, "libmx: tensor map for format %d codes failed (%d)\n", fmt, (int)r);
-    return r == CUDA_SUCCESS;
-}
-
-// Formats that kind::mxf8f6f4 multiplies (E8M0 scales on 32-element blocks),
-// and their element-type codes in its instruction descriptor.
-bool f8f6f4_fmt(int fmt) {
-    return fmt == MX_MXFP8_E4M3 || fmt == MX_MXFP8_E5M2 || fmt == MX_MXFP4 || fmt == MX_MXFP6_E3M2;
-}
-uint32_t f8f6f4_type(int fmt) {
-    switch (fmt) {
-    case MX_MXFP8_E4M3: return kTypeE4M3;
-    case MX_MXFP8_E5M2: return kTypeE5M2;
-    case MX_MXFP6_E3M2: return kTypeE3M2;
-    default: return kTypeE2M1;
-    }
-}
-// Can A and B be multiplied, and on which kernel: the format's own (same
-// format, 0..3) or the run-time-typed kind::mxf8f6f4 one.
-bool gemm_pair_ok(int fa, int fb) {
-    return (fa == fb && (fa <= MX_NVFP4 || fa == MX_MXFP4_MBS)) || (f8f6f4_fmt(fa) && f8f6f4_fmt(fb));
-}
-bool gemm_runtime_types(int fa, int fb) { return !(fa == fb && (fa <= MX_NVFP4 || fa == MX_MXFP4_MBS)); }
-bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // --- quantize ------------------------------------------------------------
 template <int FMT, int RULE = RULE_OCP>
@@ -200,21 +78,6 @@ void launch_quantize_mbs(const uint16_t *src, int64_t M, int64_t K, int64_t ld, 
                        cdiv(K / 16, 4), dst->scales + tile_bytes(MX_MXFP4_MBS, M, K));
 }
 
-// SM count of the current device, read once per device.
-int num_sms() {
-    constexpr int kMaxDev = 64;
-    static std::atomic<int> cache[kMaxDev];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const bool cached = dev >= 0 && dev < kMaxDev;
-    int n = cached ? cache[dev].load(std::memory_order_relaxed) : 0;
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-        if (cached) cache[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 mx_status launch_fused_reset(uint32_t *words, int n, cudaStream_t st);
 mx_status launch_amax_overlapped(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, float *slot, cudaStream_t st);
 
@@ -238,64 +101,7 @@ mx_status nvfp4_gscale_prepass(const uint16_t *src, int64_t M, int64_t K, int64_
     return last_launch();
 }
 
-mx_status check_tensor(const mx_tensor *t, bool need_codes) {
-    if (!t || !valid_fmt(t->fmt) || t->rows < 0 || t->cols < 0) return MX_ERR_INVALID_ARG;
-    if (t->cols % fmt_k_multiple(t->fmt) != 0) return MX_ERR_UNSUPPORTED_SHAPE;
-    if (t->rows > 0 && t->cols > 0) {
-        if (need_codes && (!t->codes || !t->scales)) return MX_ERR_INVALID_ARG;
-        if (!aligned16(t->codes) || !aligned16(t->scales)) return MX_ERR_MISALIGNED;
-        if (t->fmt == MX_NVFP4 && !t->gscale) return MX_ERR_INVALID_ARG;
-    }
-    return MX_OK;
-}
-
 // --- GEMM ----------------------------------------------------------------
-// bf16 [rows x cols] output (row pitch ld elements), box 32 x 32, no swizzle.
-bool make_tmap_c(CUtensorMap *m, void *base, int64_t rows, int64_t cols, int64_t ld) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
-    cuuint32_t box[2] = {32u, 32u};
-    cuuint32_t estr[2] = {1u, 1u};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-// Scale tiles as a 3D tensor of 8-byte words: [bands][sf_tiles_k][64] (one
-// 512-byte tile = 64 words), box = box_chunks tiles of box_bands bands.  Reads
-// past either end (a ragged K or N) return zeros.
-bool make_tmap_sf(CUtensorMap *m, const uint8_t *scales, int64_t bands, int64_t sf_tiles_k, int box_chunks,
-                  int box_bands) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {64u, (cuuint64_t)sf_tiles_k, (cuuint64_t)bands};
-    cuuint64_t strides[2] = {512u, (cuuint64_t)(sf_tiles_k * 512)};
-    cuuint32_t box[3] = {64u, (cuuint32_t)box_chunks, (cuuint32_t)box_bands};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<uint8_t *>(scales), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-// Raise the dynamic shared memory limit of kernel fn to `bytes` on the current
-// device, once per (kernel, device): the attribute belongs to the device's
-// context, so a process that drives several GPUs sets it on each.
-cudaError_t smem_limit_once(const void *fn, int bytes) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    static std::mutex mu;
-    static std::set<std::pair<const void *, int>> done;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({fn, dev}) != 0) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.insert({fn, dev});
-    return e;
-}
-
 // The activation of a fused call: bf16 x quantized inside the GEMM kernel (see
 // GemmParams::fused); A's codes and scales are its destination.
 // Room for the K split's partial sums (ksplit.cuh): the fused call's
@@ -717,21 +523,24 @@ mx_status fused_quantize_x(int fmt, const uint16_t *X, int64_t M, int64_t K, int
     return last_launch();
 }
 
+// Formats a fused call quantizes its activation to.
+bool fused_fmt(int fmt) { return valid_fmt(fmt) || fmt == MX_FP8_B128; }
+
 }  // namespace
 
 extern "C" {
 
 size_t mx_codes_bytes(int fmt, int64_t rows, int64_t cols) {
-    if (!valid_fmt(fmt) || rows < 0 || cols < 0) return 0;
+    if (!valid_fmt_any(fmt) || rows < 0 || cols < 0) return 0;
     return (size_t)(rows * cols * fmt_bits(fmt) / 8);
 }
 
 size_t mx_scales_bytes(int fmt, int64_t rows, int64_t cols) {
-    if (!valid_fmt(fmt) || rows < 0 || cols < 0) return 0;
+    if (!valid_fmt_any(fmt) || rows < 0 || cols < 0) return 0;
     return scales_bytes(fmt, rows, cols);
 }
 
-int mx_block_size(int fmt) { return valid_fmt(fmt) ? fmt_block(fmt) : 0; }
+int mx_block_size(int fmt) { return valid_fmt_any(fmt) ? fmt_block(fmt) : 0; }
 
 int mx_version(void) { return 100; }
 
@@ -769,7 +578,7 @@ mx_status mx_debug_set(int key, uint64_t value) {
 
 mx_status mx_quantize(int fmt, const void *src_bf16, int64_t M, int64_t K, int64_t ld_src, mx_tensor *dst,
                       const float *gscale_in, void *stream) {
-    if (!valid_fmt(fmt) || !dst || M < 0 || K < 0) return MX_ERR_INVALID_ARG;
+    if (!valid_fmt_any(fmt) || !dst || M < 0 || K < 0) return MX_ERR_INVALID_ARG;
     if (dst->fmt != fmt || dst->rows != M || dst->cols != K) return MX_ERR_INVALID_ARG;
     if (K % fmt_k_multiple(fmt) != 0) return MX_ERR_UNSUPPORTED_SHAPE;
     if (M == 0 || K == 0) return MX_OK;
@@ -780,6 +589,7 @@ mx_status mx_quantize(int fmt, const void *src_bf16, int64_t M, int64_t K, int64
     if (cdiv(M, kQTileRows) > 65535) return MX_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const uint16_t *src = static_cast<const uint16_t *>(src_bf16);
+    if (b128_fmt(fmt)) return quantize_b128(fmt, src, M, K, ld_src, dst, st);
     mx_status s = MX_OK;
     switch (fmt) {
     case MX_MXFP8_E4M3: s = launch_quantize<0>(src, M, K, ld_src, dst, nullptr, nullptr, st); break;
@@ -882,7 +692,7 @@ mx_status mx_quantize_rht(int fmt, const void *src_bf16, int64_t M, int64_t K, i
 mx_status mx_qsnr(const mx_tensor *q, const void *src_bf16, int64_t ld_src, double *sums, void *stream) {
     mx_status s = check_tensor(q, true);
     if (s != MX_OK) return s;
-    if (!sums) return MX_ERR_INVALID_ARG;
+    if (!sums || b128_fmt(q->fmt)) return MX_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(sums) & 7u) != 0) return MX_ERR_MISALIGNED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cudaMemsetAsync(sums, 0, 2 * sizeof(double), st) != cudaSuccess) return MX_ERR_CUDA;
@@ -915,6 +725,7 @@ mx_status mx_dequantize(const mx_tensor *src, void *dst_bf16, int64_t ld_dst, vo
     if (!dst_bf16) return MX_ERR_INVALID_ARG;
     if (ld_dst < src->cols || (ld_dst & 7) != 0 || !aligned16(dst_bf16)) return MX_ERR_MISALIGNED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (b128_fmt(src->fmt)) return dequantize_b128(src, static_cast<uint16_t *>(dst_bf16), ld_dst, st);
     const int64_t n = src->rows * (src->cols / 8);
     const unsigned blocks = (unsigned)cdiv(n, 256);
     const uint8_t *c = static_cast<const uint8_t *>(src->codes);
@@ -946,6 +757,7 @@ mx_status mx_gemm(const mx_tensor *A, const mx_tensor *B, void *C_bf16, int64_t 
     if (K == 0) return cuda_status(cudaMemset2DAsync(C_bf16, ldc * 2, 0, N * 2, M, st));
     if (K % 128 != 0) return MX_ERR_UNSUPPORTED_SHAPE;
     if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || cdiv(M, kBM) > 65535) return MX_ERR_UNSUPPORTED_SHAPE;
+    if (A->fmt == MX_FP8_B128) return gemm_b128(A, B, static_cast<uint16_t *>(C_bf16), ldc, MX_EPI_NONE, st);
     if (gemm_runtime_types(A->fmt, B->fmt) && ((fmt_bits(A->fmt) < 8 && !aligned32(A->codes)) ||
                                                (fmt_bits(B->fmt) < 8 && !aligned32(B->codes))))
         return MX_ERR_MISALIGNED;
@@ -955,12 +767,12 @@ mx_status mx_gemm(const mx_tensor *A, const mx_tensor *B, void *C_bf16, int64_t 
 }
 
 size_t mx_fused_workspace_bytes(int fmt, int64_t M, int64_t K) {
-    if (!valid_fmt(fmt) || M < 0 || K < 0 || M > INT32_MAX || K > INT32_MAX) return 0;
+    if (!fused_fmt(fmt) || M < 0 || K < 0 || M > INT32_MAX || K > INT32_MAX) return 0;
     return fused_ws_bytes(fmt, M, K);
 }
 
 size_t mx_fused_split_workspace_bytes(int fmt, int64_t M, int64_t K) {
-    if (!valid_fmt(fmt) || M < 0 || K < 0 || M > INT32_MAX || K > INT32_MAX) return 0;
+    if (!fused_fmt(fmt) || M < 0 || K < 0 || M > INT32_MAX || K > INT32_MAX) return 0;
     return fused_ws_split_bytes(fmt, M, K);
 }
 
@@ -986,7 +798,7 @@ int mx_debug_split_units(int64_t tiles, int workers, int kt, int mode, int worke
 mx_status mx_gemm_fused_act(int fmt, const void *X_bf16, int64_t M, int64_t K, int64_t ldx, const mx_tensor *W,
                             void *C_bf16, int64_t ldc, int epilogue, float *amax_out, const float *x_gscale,
                             const float *x_amax, void *workspace, size_t workspace_bytes, void *stream) {
-    if (!valid_fmt(fmt) || M < 0 || K < 0) return MX_ERR_INVALID_ARG;
+    if (!fused_fmt(fmt) || M < 0 || K < 0) return MX_ERR_INVALID_ARG;
     mx_status s = check_tensor(W, true);
     if (s != MX_OK) return s;
     if (!gemm_pair_ok(fmt, W->fmt) || W->cols != K) return MX_ERR_INVALID_ARG;
@@ -1026,6 +838,20 @@ mx_status mx_gemm_fused_act(int fmt, const void *X_bf16, int64_t M, int64_t K, i
         s = last_launch();
         if (s != MX_OK) return s;
         return launch_gemm_mbs(&xa, W, static_cast<uint16_t *>(C_bf16), ldc, st);
+    }
+    if (fmt == MX_FP8_B128) {
+        // the quantize, then the block-128 GEMM in stream order; |C| max is not taken
+        if (amax_out != nullptr) return MX_ERR_INVALID_ARG;
+        xa.fmt = fmt;
+        xa.reserved = 0;
+        xa.rows = M;
+        xa.cols = K;
+        xa.codes = ws + fused_ws_header(M);
+        xa.scales = ws + fused_ws_header(M) + align256((size_t)(M * K));
+        xa.gscale = nullptr;
+        s = quantize_b128(fmt, X, M, K, ldx, &xa, st);
+        if (s != MX_OK) return s;
+        return gemm_b128(&xa, W, static_cast<uint16_t *>(C_bf16), ldc, epilogue, st);
     }
     // room for the K split's partial sums (the GEMM decides whether to split)
     SplitRoom room;
@@ -1141,7 +967,7 @@ extern "C" {
 mx_status mx_gemm_fused_act_noalloc(int fmt, const void *X_bf16, int64_t M, int64_t K, int64_t ldx,
                                     const mx_tensor *W, void *C_bf16, int64_t ldc, int epilogue, float *amax_out,
                                     const float *x_gscale, const float *x_amax, void *stream) {
-    if (!valid_fmt(fmt) || M < 0 || K < 0) return MX_ERR_INVALID_ARG;
+    if (!fused_fmt(fmt) || M < 0 || K < 0) return MX_ERR_INVALID_ARG;
     // sizes the fused call rejects anyway, checked first so that the byte
     // count below cannot overflow
     if (M > INT32_MAX || K > INT32_MAX || cdiv(M, kBM) > 65535) return MX_ERR_UNSUPPORTED_SHAPE;
@@ -1164,6 +990,14 @@ mx_status mx_check_device_error(void *stream, uint32_t info[4]) {
     if (cudaMemcpyFromSymbol(w, g_error_word, sizeof(w)) != cudaSuccess) return MX_ERR_CUDA;
     const uint32_t zero[4] = {0, 0, 0, 0};
     if (cudaMemcpyToSymbol(g_error_word, zero, sizeof(zero)) != cudaSuccess) return MX_ERR_CUDA;
+    uint32_t x[4] = {0, 0, 0, 0};
+    if (experts_error_word(x) != MX_OK) return MX_ERR_CUDA;
+    if (w[3] == 0) {   // the first site of the kernels that reported one
+        w[1] = x[1];
+        w[2] = x[2];
+    }
+    w[0] |= x[0];
+    w[3] += x[3];
     if (info) memcpy(info, w, sizeof(w));
     if (w[0] & DEVERR_TIMEOUT) return MX_ERR_TIMEOUT;
     if (w[0] & DEVERR_BOUNDS) return MX_ERR_DEVICE;

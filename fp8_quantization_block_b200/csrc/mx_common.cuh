@@ -333,6 +333,30 @@ MX_DEVICE_INLINE void tc_mma_nvf4(uint32_t d, uint64_t adesc, uint64_t bdesc, ui
         : "memory");
 }
 
+// FP8 MMAs without block scales (kind::f8f6f4), issued by the threads whose
+// `issue` flag is set; the whole warp executes them with uniform operands.
+#define MX_DEFINE_F8_MMA_IF(NAME, GROUP)                                                                             \
+    MX_DEVICE_INLINE void NAME(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,     \
+                               uint32_t issue) {                                                                     \
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"                   \
+                     "@q tcgen05.mma.cta_group::" GROUP ".kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),         \
+                     "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue)                                  \
+                     : "memory");                                                                                    \
+    }
+MX_DEFINE_F8_MMA_IF(tc_mma_f8_if, "1")
+MX_DEFINE_F8_MMA_IF(tc_mma_pair_f8_if, "2")
+#undef MX_DEFINE_F8_MMA_IF
+
+// Register split between warpgroups: all four warps of a warpgroup execute it.
+template <int N>
+MX_DEVICE_INLINE void setmaxnreg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+MX_DEVICE_INLINE void setmaxnreg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Load 32 consecutive fp32 columns of this warp's 32 TMEM lanes (one row per thread).
 MX_DEVICE_INLINE void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(

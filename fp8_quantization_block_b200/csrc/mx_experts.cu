@@ -1,0 +1,451 @@
+// mx_experts.cu -- the block-128 FP8 formats and the operators of a mixture of
+// experts: host-side checks, tensor maps and launches of quantize_b128.cuh,
+// gemm_b128_sm100.cuh, gemm_grouped_sm100.cuh and routing.cuh.  A translation
+// unit of its own, so that the other GEMMs need not be compiled with it.
+#include <cstring>
+
+#include "gemm_b128_sm100.cuh"
+#include "gemm_grouped_sm100.cuh"
+#include "mx_host.cuh"
+#include "quantize_b128.cuh"
+#include "routing.cuh"
+
+namespace mx {
+
+namespace {
+
+cudaLaunchConfig_t launch_cfg(dim3 grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = (unsigned)pdl_attr(attr);
+    return cfg;
+}
+
+// --- tiles of the block-128 GEMM ------------------------------------------------
+struct B128Config {
+    bool pair;
+    int bm_shift;   // log2 of the tile's rows
+    int bn;
+};
+
+// The tile with the shortest run: waves of tiles times the tensor cycles of a
+// tile's K block (2 bn, whatever its rows up to 128, or 256 on a pair of CTAs)
+// plus what a block costs beside them (kBlockCycles: barriers, the drain's
+// latency).  m_blocks(rows) counts the row blocks of that height.
+template <typename MBlocks>
+B128Config b128_config(int64_t n, int sms, bool allow_pair, int max_shift, MBlocks m_blocks) {
+    constexpr double kBlockCycles = 64.0;
+    B128Config best{false, max_shift < 7 ? max_shift : 7, 256};
+    double best_cost = 1e300;
+    for (int pair = 0; pair <= (allow_pair ? 1 : 0); ++pair) {
+        const int shift = pair ? 8 : best.bm_shift;
+        const int64_t workers = pair ? sms / 2 : sms;
+        for (int bn = 256; bn >= 32; bn -= 32) {
+            const int64_t tiles = m_blocks(1 << shift) * cdiv(n, bn);
+            const double cost = (double)cdiv(tiles, workers) * (2.0 * bn + kBlockCycles);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = B128Config{pair != 0, shift, bn};
+            }
+        }
+    }
+    return best;
+}
+
+template <bool PAIR, int CH, bool GROUPED>
+mx_status launch_b128_t(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc, const B128GemmParams &p,
+                        int workers, size_t smem, cudaStream_t st) {
+    const auto kern = gemm_b128_kernel<PAIR, CH, GROUPED>;
+    if (smem_limit_once(reinterpret_cast<const void *>(kern), kSmemLimit) != cudaSuccess) return MX_ERR_CUDA;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(PAIR ? 2 * workers : workers), 1, 1), kB128Threads, smem, st, attr);
+    if (PAIR) {
+        cudaLaunchAttribute &c = attr[cfg.numAttrs++];
+        c.id = cudaLaunchAttributeClusterDimension;
+        c.val.clusterDim.x = 2;
+        c.val.clusterDim.y = 1;
+        c.val.clusterDim.z = 1;
+    }
+    cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, p);
+    return last_launch();
+}
+
+// A x B (groups == nullptr: one product of all rows).
+mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_groups *groups, uint16_t *C, int64_t ldc,
+                           int epilogue, cudaStream_t st) {
+    const int64_t M = A->rows, N = B->rows, K = A->cols;
+    const int64_t G = groups ? groups->count : 1;
+    const int sms = num_sms();
+    const int cap = g_max_gemm_ctas.load();
+    B128Config cfg;
+    if (groups) {
+        // sizes of the groups are device data: their mean decides
+        const int64_t mean = cdiv(M, G);
+        const int shift = mean <= 24 ? 5 : (mean <= 48 ? 6 : 7);
+        cfg = b128_config(N, sms, mean > 192 && N > 128 && g_pair_enabled.load(), shift, [&](int64_t bm) {
+            return (G < M ? G : M) / 2 + cdiv(M, bm);   // half a block of each group is ragged
+        });
+    } else {
+        const int shift = M <= 32 ? 5 : (M <= 64 ? 6 : 7);
+        cfg = b128_config(N, sms, M > 128 && N > 128 && g_pair_enabled.load(), shift,
+                          [&](int64_t bm) { return cdiv(M, bm); });
+    }
+    B128GemmParams p{};
+    const int a_rows = cfg.pair ? 128 : 1 << cfg.bm_shift;
+    const int b_rows = cfg.pair ? cfg.bn / 2 : cfg.bn;
+    p.a_bytes = a_rows * kStageKBytes;
+    p.b_bytes = b_rows * kStageKBytes;
+    const int fixed = 1024 + kB128StagingBytes + (2 * kB128MaxStages + 9) * 8 + 16;
+    p.stages = (kSmemLimit - fixed) / (p.a_bytes + p.b_bytes);
+    if (p.stages > kB128MaxStages) p.stages = kB128MaxStages;
+    const size_t smem = (size_t)fixed + (size_t)p.stages * (p.a_bytes + p.b_bytes);
+    CUtensorMap ta, tb, tc;
+    if (!make_tmap_u8(&ta, A->codes, M, K, a_rows)) return MX_ERR_CUDA;
+    if (!make_tmap_u8(&tb, B->codes, G * N, K, b_rows)) return MX_ERR_CUDA;
+    const bool tma_store = (ldc % 8 == 0) && aligned16(C);
+    memset(&tc, 0, sizeof(tc));
+    if (tma_store && !make_tmap_c(&tc, C, M, N, ldc)) return MX_ERR_CUDA;
+    p.sa = reinterpret_cast<const float *>(A->scales);
+    p.sb = reinterpret_cast<const float *>(B->scales);
+    p.C = C;
+    p.ldc = ldc;
+    p.sa_pitch = b128_pitch(M);
+    p.sb_step = (int64_t)(scales_bytes(MX_FP8_B128X128, N, K) / 4);
+    p.M = (int)M;
+    p.N = (int)N;
+    p.num_kb = (int)(K / 128);
+    p.bm_shift = cfg.bm_shift;
+    p.bn = cfg.bn;
+    p.m_blocks = (int)cdiv(M, (int64_t)1 << cfg.bm_shift);
+    p.n_blocks = (int)cdiv(N, cfg.bn);
+    p.epilogue = epilogue;
+    p.use_tma_store = tma_store ? 1 : 0;
+    p.skip_producer = g_skip_producer.load();
+    p.wait_limit_ns = g_wait_limit_ns.load();
+    if (groups) p.groups = Groups{groups->offsets, groups->count, (int)M};
+    // an upper bound of the tiles: a ragged block per group
+    const int64_t blocks = groups ? (M < (M >> cfg.bm_shift) + G ? M : (M >> cfg.bm_shift) + G) : p.m_blocks;
+    const int64_t tiles = blocks * p.n_blocks;
+    if (tiles > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
+    int64_t workers = cfg.pair ? sms / 2 : sms;
+    if (cap > 0 && cap < sms) workers = cfg.pair ? (cap + 1) / 2 : cap;
+    if (workers > tiles) workers = tiles;
+    const bool wide = cfg.bn > 128;
+#define MX_LAUNCH(PAIR, CH)                                                                             \
+    return groups ? launch_b128_t<PAIR, CH, true>(ta, tb, tc, p, (int)workers, smem, st)               \
+                  : launch_b128_t<PAIR, CH, false>(ta, tb, tc, p, (int)workers, smem, st)
+    if (cfg.pair) {
+        if (wide) MX_LAUNCH(true, 4);
+        MX_LAUNCH(true, 2);
+    }
+    if (wide) MX_LAUNCH(false, 4);
+    MX_LAUNCH(false, 2);
+#undef MX_LAUNCH
+}
+
+template <int FMT>
+mx_status launch_grouped_t(const mx_tensor *A, const mx_tensor *B, const mx_groups *groups, uint16_t *C, int64_t ldc,
+                           int epilogue, cudaStream_t st) {
+    constexpr int BN = 256, kStages = 4;
+    using L = GemmSmem<FMT, BN, kStages>;
+    const int64_t M = A->rows, N = B->rows, K = A->cols, G = groups->count;
+    const int64_t kbytes = K / GemmFmt<FMT>::kElemPerByte;
+    const int64_t sf_tiles_k = cdiv(K / fmt_block(A->fmt), 4);
+    const int64_t bands = group_bands(M, G);
+    CUtensorMap ta, tb, tc, tsa, tsb;
+    if (FMT == kGemmRuntimeTypes) {
+        if (!make_tmap_codes_f8f6f4(&ta, A->fmt, A->codes, M, K, kBM)) return MX_ERR_CUDA;
+        if (!make_tmap_codes_f8f6f4(&tb, B->fmt, B->codes, G * N, K, BN)) return MX_ERR_CUDA;
+    } else {
+        if (!make_tmap_u8(&ta, A->codes, M, kbytes, kBM)) return MX_ERR_CUDA;
+        if (!make_tmap_u8(&tb, B->codes, G * N, kbytes, BN)) return MX_ERR_CUDA;
+    }
+    if (!make_tmap_sf(&tsa, A->scales, bands, sf_tiles_k, kSfGroup * GemmFmt<FMT>::kChunks, 1)) return MX_ERR_CUDA;
+    if (!make_tmap_sf(&tsb, B->scales, G * cdiv(N, 128), sf_tiles_k, kSfGroup * GemmFmt<FMT>::kChunks, L::kBBands))
+        return MX_ERR_CUDA;
+    const bool tma_store = (ldc % 8 == 0) && aligned16(C);
+    memset(&tc, 0, sizeof(tc));
+    if (tma_store && !make_tmap_c(&tc, C, M, N, ldc)) return MX_ERR_CUDA;
+    const auto kern = gemm_grouped_kernel<FMT, kStages>;
+    if (smem_limit_once(reinterpret_cast<const void *>(kern), L::kAlloc) != cudaSuccess) return MX_ERR_CUDA;
+    GemmParams p{};
+    p.sf_tiles_k = sf_tiles_k;
+    p.C = C;
+    p.ldc = ldc;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.num_kt = (int)cdiv(kbytes, kStageKBytes);
+    p.n_blocks = (int)cdiv(N, BN);
+    p.ga = A->gscale;
+    p.gb = B->gscale;
+    p.epilogue = epilogue;
+    p.use_tma_store = tma_store ? 1 : 0;
+    p.skip_producer = g_skip_producer.load();
+    p.ab_types = (f8f6f4_type(A->fmt) << 7) | (f8f6f4_type(B->fmt) << 10);
+    p.stage_tx = (uint32_t)(kStageKBytes * (kBM * fmt_bits(A->fmt) + BN * fmt_bits(B->fmt)) / 8);
+    p.wait_limit_ns = g_wait_limit_ns.load();
+    const int64_t tiles = bands * p.n_blocks;
+    if (tiles > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
+    const int cap = g_max_gemm_ctas.load();
+    int64_t grid = cap > 0 && cap < num_sms() ? cap : num_sms();
+    if (grid > tiles) grid = tiles;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)grid, 1, 1), kGemmThreads, L::kAlloc, st, attr);
+    cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, tsa, tsb, p, Groups{groups->offsets, groups->count, (int)M});
+    return last_launch();
+}
+
+mx_status check_groups(const mx_groups *g) {
+    if (!g || g->count < 1 || !g->offsets) return MX_ERR_INVALID_ARG;
+    if (g->count > MX_MAX_GROUPS) return MX_ERR_UNSUPPORTED_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(g->offsets) & 3u) != 0) return MX_ERR_MISALIGNED;
+    return MX_OK;
+}
+
+template <int FMT>
+void launch_quantize_grouped(const GroupedQuantParams &p, int64_t bands, cudaStream_t st) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)cdiv(p.K, kQTileCols), (unsigned)bands, 1), kQThreads, 0, st, attr);
+    cudaLaunchKernelEx(&cfg, quantize_grouped_kernel<FMT>, p);
+}
+
+template <typename ID>
+mx_status launch_route(const RouteParams &p, cudaStream_t st) {
+    cudaLaunchAttribute attr[1];
+    const size_t smem = (size_t)kRouteWarps * p.groups * sizeof(int);
+    const int limit = kRouteWarps * kRouteMaxGroups * (int)sizeof(int);
+    if (p.n <= kRouteChunk) {
+        if (smem_limit_once(reinterpret_cast<const void *>(route_small_kernel<ID>), limit) != cudaSuccess)
+            return MX_ERR_CUDA;
+        cudaLaunchConfig_t cfg = launch_cfg(dim3(1, 1, 1), kRouteThreads, smem, st, attr);
+        cudaLaunchKernelEx(&cfg, route_small_kernel<ID>, p);
+        return last_launch();
+    }
+    if (smem_limit_once(reinterpret_cast<const void *>(route_count_kernel<ID>), limit) != cudaSuccess ||
+        smem_limit_once(reinterpret_cast<const void *>(route_place_kernel<ID>), limit) != cudaSuccess)
+        return MX_ERR_CUDA;
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)p.chunks, 1, 1), kRouteThreads, smem, st, attr);
+    cudaLaunchKernelEx(&cfg, route_count_kernel<ID>, p);
+    cudaLaunchConfig_t one = launch_cfg(dim3(1, 1, 1), kRouteThreads, 0, st, attr);
+    cudaLaunchKernelEx(&one, route_scan_kernel, p);
+    cudaLaunchKernelEx(&cfg, route_place_kernel<ID>, p);
+    return last_launch();
+}
+
+}  // namespace
+
+// --- entries used by mx_api.cu ----------------------------------------------------
+mx_status quantize_b128(int fmt, const uint16_t *src, int64_t M, int64_t K, int64_t ld, const mx_tensor *dst,
+                        cudaStream_t st) {
+    B128QuantParams p{};
+    p.src = src;
+    p.ld = ld;
+    p.src_rows = M;
+    p.M = M;
+    p.K = K;
+    p.codes = static_cast<uint8_t *>(dst->codes);
+    p.scales = reinterpret_cast<float *>(dst->scales);
+    p.pitch = fmt == MX_FP8_B128 ? b128_pitch(M) : K / 128;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(K / 128), (unsigned)cdiv(M, kQTileRows), 1), kQThreads, 0, st, attr);
+    if (fmt == MX_FP8_B128) cudaLaunchKernelEx(&cfg, quantize_b128_kernel<false, false>, p);
+    else cudaLaunchKernelEx(&cfg, quantize_b128_kernel<true, false>, p);
+    return last_launch();
+}
+
+mx_status dequantize_b128(const mx_tensor *src, uint16_t *dst, int64_t ld, cudaStream_t st) {
+    const int64_t n = src->rows * (src->cols / 8);
+    if (cdiv(n, 256) > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
+    const bool rows = src->fmt == MX_FP8_B128;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)cdiv(n, 256), 1, 1), 256, 0, st, attr);
+    cudaLaunchKernelEx(&cfg, dequantize_b128_kernel, static_cast<const uint8_t *>(src->codes),
+                       reinterpret_cast<const float *>(src->scales), src->rows, src->cols, (int64_t)(rows ? 1 : 128),
+                       rows ? (int64_t)1 : src->cols / 128, rows ? b128_pitch(src->rows) : (int64_t)1, dst, ld);
+    return last_launch();
+}
+
+mx_status gemm_b128(const mx_tensor *A, const mx_tensor *B, uint16_t *C, int64_t ldc, int epilogue, cudaStream_t st) {
+    return launch_gemm_b128(A, B, nullptr, C, ldc, epilogue, st);
+}
+
+// This unit's device error word (each translation unit has its own).
+mx_status experts_error_word(uint32_t w[4]) {
+    const uint32_t zero[4] = {0, 0, 0, 0};
+    if (cudaMemcpyFromSymbol(w, g_error_word, sizeof(zero)) != cudaSuccess) return MX_ERR_CUDA;
+    if (cudaMemcpyToSymbol(g_error_word, zero, sizeof(zero)) != cudaSuccess) return MX_ERR_CUDA;
+    return MX_OK;
+}
+
+}  // namespace mx
+
+using namespace mx;
+
+extern "C" {
+
+size_t mx_grouped_scales_bytes(int fmt, int64_t rows, int64_t groups, int64_t cols) {
+    if (!valid_fmt_any(fmt) || fmt == MX_MXFP4_MBS || fmt == MX_FP8_B128X128 || rows < 0 || groups < 0 || cols < 0)
+        return 0;
+    if (fmt == MX_FP8_B128) return scales_bytes(fmt, rows, cols);
+    return scales_bytes(fmt, group_bands(rows, groups) * 128, cols);
+}
+
+mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, int64_t K, int64_t ld_src,
+                              const int32_t *row_index, const mx_groups *groups, mx_tensor *dst,
+                              const float *gscale_in, void *stream) {
+    if (!valid_fmt_any(fmt) || fmt == MX_MXFP4_MBS || fmt == MX_FP8_B128X128 || !dst || src_rows < 0 || K < 0)
+        return MX_ERR_INVALID_ARG;
+    mx_status s = check_groups(groups);
+    if (s != MX_OK) return s;
+    if (dst->fmt != fmt || dst->cols != K || dst->rows < 0) return MX_ERR_INVALID_ARG;
+    const int64_t T = dst->rows;
+    if (row_index == nullptr && src_rows < T) return MX_ERR_INVALID_ARG;
+    if (K % fmt_k_multiple(fmt) != 0) return MX_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0 || K == 0) return MX_OK;
+    if (!src_bf16 || !dst->codes || !dst->scales) return MX_ERR_INVALID_ARG;
+    if (fmt == MX_NVFP4 && !gscale_in) return MX_ERR_INVALID_ARG;
+    if (ld_src < K || (ld_src & 7) != 0) return MX_ERR_MISALIGNED;
+    if (!aligned16(src_bf16) || !aligned16(dst->codes) || !aligned16(dst->scales)) return MX_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(row_index) & 3u) != 0) return MX_ERR_MISALIGNED;
+    const int64_t bands = fmt == MX_FP8_B128 ? cdiv(T, kQTileRows) : group_bands(T, groups->count);
+    if (T > INT32_MAX || bands > 65535) return MX_ERR_UNSUPPORTED_SHAPE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (fmt == MX_FP8_B128) {
+        B128QuantParams p{};
+        p.src = static_cast<const uint16_t *>(src_bf16);
+        p.ld = ld_src;
+        p.src_rows = src_rows;
+        p.row_index = row_index;
+        p.offsets = groups->offsets;
+        p.groups = groups->count;
+        p.M = T;
+        p.K = K;
+        p.codes = static_cast<uint8_t *>(dst->codes);
+        p.scales = reinterpret_cast<float *>(dst->scales);
+        p.pitch = b128_pitch(T);
+        cudaLaunchAttribute attr[1];
+        cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(K / 128), (unsigned)bands, 1), kQThreads, 0, st, attr);
+        cudaLaunchKernelEx(&cfg, quantize_b128_kernel<false, true>, p);
+        return last_launch();
+    }
+    GroupedQuantParams p{};
+    p.src = static_cast<const uint16_t *>(src_bf16);
+    p.ld = ld_src;
+    p.src_rows = src_rows;
+    p.row_index = row_index;
+    p.groups = Groups{groups->offsets, groups->count, (int)T};
+    p.K = K;
+    p.codes = static_cast<uint8_t *>(dst->codes);
+    p.scales = dst->scales;
+    p.sf_tiles_k = cdiv(K / fmt_block(fmt), 4);
+    p.gscale = gscale_in;
+    p.gscale_out = gscale_in == dst->gscale ? nullptr : dst->gscale;
+    switch (fmt) {
+    case MX_MXFP8_E4M3: launch_quantize_grouped<FMT_E4M3>(p, bands, st); break;
+    case MX_MXFP8_E5M2: launch_quantize_grouped<FMT_E5M2>(p, bands, st); break;
+    case MX_MXFP4: launch_quantize_grouped<FMT_MXFP4>(p, bands, st); break;
+    case MX_MXFP6_E3M2: launch_quantize_grouped<FMT_MXFP6>(p, bands, st); break;
+    default: launch_quantize_grouped<FMT_NVFP4>(p, bands, st);
+    }
+    return last_launch();
+}
+
+mx_status mx_gemm_grouped(const mx_tensor *A, const mx_tensor *B, const mx_groups *groups, void *C_bf16, int64_t ldc,
+                          int epilogue, void *stream) {
+    mx_status s = check_tensor(A, true);
+    if (s != MX_OK) return s;
+    s = check_tensor(B, true);
+    if (s != MX_OK) return s;
+    s = check_groups(groups);
+    if (s != MX_OK) return s;
+    if (!gemm_pair_ok(A->fmt, B->fmt) || A->fmt == MX_MXFP4_MBS || A->cols != B->cols) return MX_ERR_INVALID_ARG;
+    if (epilogue != MX_EPI_NONE && epilogue != MX_EPI_GELU) return MX_ERR_INVALID_ARG;
+    const int64_t M = A->rows, N = B->rows, K = A->cols;
+    if (M == 0 || N == 0) return MX_OK;
+    if (!C_bf16 || ldc < N) return MX_ERR_INVALID_ARG;
+    if (!aligned16(C_bf16)) return MX_ERR_MISALIGNED;
+    if (K == 0 || K % 128 != 0) return MX_ERR_UNSUPPORTED_SHAPE;
+    if (M > INT32_MAX || K > INT32_MAX || groups->count * N > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
+    const bool runtime = A->fmt != MX_FP8_B128 && (gemm_runtime_types(A->fmt, B->fmt) || A->fmt == MX_MXFP8_E5M2);
+    if (runtime && ((fmt_bits(A->fmt) < 8 && !aligned32(A->codes)) || (fmt_bits(B->fmt) < 8 && !aligned32(B->codes))))
+        return MX_ERR_MISALIGNED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint16_t *C = static_cast<uint16_t *>(C_bf16);
+    if (A->fmt == MX_FP8_B128) return launch_gemm_b128(A, B, groups, C, ldc, epilogue, st);
+    if (runtime) return launch_grouped_t<kGemmRuntimeTypes>(A, B, groups, C, ldc, epilogue, st);
+    switch (A->fmt) {
+    case MX_MXFP8_E4M3: return launch_grouped_t<0>(A, B, groups, C, ldc, epilogue, st);
+    case MX_MXFP4: return launch_grouped_t<2>(A, B, groups, C, ldc, epilogue, st);
+    default: return launch_grouped_t<3>(A, B, groups, C, ldc, epilogue, st);
+    }
+}
+
+size_t mx_route_workspace_bytes(int64_t tokens, int choices, int groups) {
+    if (tokens < 0 || choices < 1 || groups < 1 || tokens > INT32_MAX / choices) return 0;
+    const int64_t n = tokens * choices;
+    return n <= kRouteChunk ? 0 : (size_t)(cdiv(n, kRouteChunk) * groups) * sizeof(int32_t);
+}
+
+mx_status mx_route(const void *ids, int id_bits, int64_t tokens, int choices, int groups, int32_t *offsets,
+                   int32_t *row_token, int32_t *slot, void *workspace, size_t workspace_bytes, void *stream) {
+    if ((id_bits != 32 && id_bits != 64) || tokens < 0 || choices < 1 || groups < 1) return MX_ERR_INVALID_ARG;
+    if (groups > MX_MAX_GROUPS || tokens > INT32_MAX / choices) return MX_ERR_UNSUPPORTED_SHAPE;
+    if (!offsets) return MX_ERR_INVALID_ARG;
+    if (tokens > 0 && (!ids || !row_token || !slot)) return MX_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ids) & (id_bits / 8 - 1)) != 0 ||
+        ((reinterpret_cast<uintptr_t>(offsets) | reinterpret_cast<uintptr_t>(row_token) |
+          reinterpret_cast<uintptr_t>(slot) | reinterpret_cast<uintptr_t>(workspace)) & 3u) != 0)
+        return MX_ERR_MISALIGNED;
+    const size_t need = mx_route_workspace_bytes(tokens, choices, groups);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MX_ERR_INVALID_ARG;
+    RouteParams p{};
+    p.ids = ids;
+    p.n = tokens * choices;
+    p.choices = choices;
+    p.groups = groups;
+    p.offsets = offsets;
+    p.row_token = row_token;
+    p.slot = slot;
+    p.counts = static_cast<int32_t *>(workspace);
+    p.chunks = (int)cdiv(p.n, kRouteChunk);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return id_bits == 32 ? launch_route<int32_t>(p, st) : launch_route<int64_t>(p, st);
+}
+
+mx_status mx_combine(const void *Y_bf16, int64_t rows, int64_t cols, int64_t ldy, const int32_t *slot,
+                     const float *weights, int64_t tokens, int choices, void *out_bf16, int64_t ldo, void *stream) {
+    if (rows < 0 || cols < 0 || tokens < 0 || choices < 1) return MX_ERR_INVALID_ARG;
+    if (tokens == 0 || cols == 0) return MX_OK;
+    if ((rows > 0 && !Y_bf16) || !slot || !weights || !out_bf16 || ldy < cols || ldo < cols) return MX_ERR_INVALID_ARG;
+    if (tokens > INT32_MAX / choices || rows > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
+    if (((reinterpret_cast<uintptr_t>(Y_bf16) | reinterpret_cast<uintptr_t>(out_bf16)) & 1u) != 0 ||
+        ((reinterpret_cast<uintptr_t>(slot) | reinterpret_cast<uintptr_t>(weights)) & 3u) != 0)
+        return MX_ERR_MISALIGNED;
+    CombineParams p{};
+    p.y = static_cast<const uint16_t *>(Y_bf16);
+    p.ldy = ldy;
+    p.rows = rows;
+    p.slot = slot;
+    p.weights = weights;
+    p.choices = choices;
+    p.cols = cols;
+    p.out = static_cast<uint16_t *>(out_bf16);
+    p.ldo = ldo;
+    // 16-byte accesses where every row starts on one; the columns then come in whole vectors
+    const bool vec = cols % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0 && aligned16(Y_bf16) && aligned16(out_bf16);
+    const int64_t chunks = cdiv(cols, 256 * (vec ? 8 : 1));
+    if (chunks > 65535) return MX_ERR_UNSUPPORTED_SHAPE;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)tokens, (unsigned)chunks, 1), 256, 0,
+                                        static_cast<cudaStream_t>(stream), attr);
+    if (vec) cudaLaunchKernelEx(&cfg, combine_kernel<8>, p);
+    else cudaLaunchKernelEx(&cfg, combine_kernel<1>, p);
+    return last_launch();
+}
+
+}  // extern "C"

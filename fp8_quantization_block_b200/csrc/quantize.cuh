@@ -729,7 +729,7 @@ struct MbsTables {
 // Elements: v = x 2^(135-E) (two exact power-of-two products), code = RNE of
 // v / (256 + m) on E2M1 by the directed-rounding bracket, ties settled exactly.
 // macro_out: the [M][K/128] macro mantissa bytes (K % 128 == 0).
-__global__ void __launch_bounds__(kQThreads) quantize_mbs_kernel(const uint16_t *__restrict__ src, int64_t M,
+static __global__ void __launch_bounds__(kQThreads) quantize_mbs_kernel(const uint16_t *__restrict__ src, int64_t M,
                                                                  int64_t K, int64_t ld, uint8_t *__restrict__ codes,
                                                                  uint8_t *__restrict__ scales, int64_t sf_tiles_k,
                                                                  uint8_t *__restrict__ macro_out) {
@@ -846,7 +846,7 @@ MX_DEVICE_INLINE uint32_t mbs_dyn_code(double a, double denom) {
     return c;
 }
 
-__global__ void __launch_bounds__(256) quantize_mbs_dynamic_kernel(const uint16_t *__restrict__ src, int64_t M,
+static __global__ void __launch_bounds__(256) quantize_mbs_dynamic_kernel(const uint16_t *__restrict__ src, int64_t M,
                                                                   int64_t K, int64_t ld,
                                                                   uint8_t *__restrict__ codes,
                                                                   uint8_t *__restrict__ scales, int64_t sf_tiles_k,
@@ -942,7 +942,7 @@ __global__ void __launch_bounds__(256) quantize_mbs_dynamic_kernel(const uint16_
 // quantize_kernel) before reducing them.  Walking the tiles from the end of the
 // tensor towards its start leaves the first rows in L2 when the pass ends, and
 // the quantize kernel that follows reads those rows first.
-__global__ void __launch_bounds__(kQThreads) amax_kernel(const uint16_t *__restrict__ src, int64_t M, int64_t K,
+static __global__ void __launch_bounds__(kQThreads) amax_kernel(const uint16_t *__restrict__ src, int64_t M, int64_t K,
                                                          int64_t ld, unsigned int *__restrict__ amax_bits) {
     // src and the zeroed slot may come from the previous kernel in the stream
     // (launched with programmatic serialization, this kernel starts early);
@@ -994,7 +994,7 @@ inline int64_t amax_grid(int64_t M, int64_t K, int num_sms) {
 // g = RU_fp32(amax / 2688), 1 for an all-zero tensor; in place (amax bits -> g).
 // Launched with programmatic serialization, it waits for the amax pass before
 // reading the slot, and lets the quantize kernel launch at once.
-__global__ void gscale_from_amax_kernel(float *__restrict__ slot) {
+static __global__ void gscale_from_amax_kernel(float *__restrict__ slot) {
     griddep_wait();
     griddep_launch_dependents();
     const float amax = *slot;

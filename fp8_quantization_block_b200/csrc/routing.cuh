@@ -1,0 +1,261 @@
+// routing.cuh -- the two ends of a mixture of experts: from the experts chosen
+// for each token to rows grouped by expert, and from the experts' output rows
+// back to tokens.
+//
+// Route: n = tokens x choices ids; slot of a choice = its place when all
+// choices are sorted by expert, stably (by token, then choice):
+//   offsets[g] = number of choices with an expert below g,
+//   slot(i) = offsets[id_i] + |{j < i : id_j = id_i}|,
+// ids outside [0, groups) have no slot.  A counting sort with no atomics on
+// shared counters in the placing step, so the order never varies: every warp
+// owns a contiguous run of choices, counts it per expert, takes the counts of
+// the warps before it as its bases, and then places 32 choices at a time, the
+// rank within the 32 from __match_any_sync.
+//
+// Combine: out[t] = RNE_bf16(sum_j w[t][j] Y[slot[t][j]]), FP32, j ascending.
+#pragma once
+
+#include "mx_common.cuh"
+#include "quantize.cuh"
+
+namespace mx {
+
+constexpr int kRouteThreads = 1024;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteMaxGroups = 1024;
+constexpr int kRouteChunk = 8192;   // choices per CTA; up to this many, one CTA does it all
+
+struct RouteParams {
+    const void *ids;          // int32 or int64 [n]
+    int64_t n;
+    int choices;
+    int groups;
+    int32_t *offsets;         // [groups + 1]
+    int32_t *row_token;       // [n]
+    int32_t *slot;            // [n]
+    int32_t *counts;          // workspace: [groups][chunks], then their exclusive prefix sums
+    int chunks;
+};
+
+template <typename ID>
+MX_DEVICE_INLINE int route_id(const RouteParams &p, int64_t i, int64_t end) {
+    if (i >= end) return -1;
+    const ID v = static_cast<const ID *>(p.ids)[i];
+    return v >= 0 && v < (ID)p.groups ? (int)v : -1;
+}
+
+// Exclusive prefix sum of one value per thread over the CTA (warp_sums: 32 ints).
+MX_DEVICE_INLINE int block_exclusive(int v, int *warp_sums, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = lane < (int)(blockDim.x / 32) ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[31];
+    return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+// Per-warp counts of this CTA's choices into cnt[warp][groups].
+template <typename ID>
+MX_DEVICE_INLINE void route_count(const RouteParams &p, int64_t begin, int64_t end, int64_t per_warp, int *cnt) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < kRouteWarps * p.groups; i += kRouteThreads) cnt[i] = 0;
+    __syncthreads();
+    const int64_t w0 = begin + warp * per_warp, w1 = min(w0 + per_warp, end);
+    for (int64_t i = w0; i < w1; i += 32) {
+        const int g = route_id<ID>(p, i + lane, w1);
+        const uint32_t same = __match_any_sync(0xffffffffu, g);
+        if (g >= 0 && (__ffs(same) - 1) == lane) cnt[warp * p.groups + g] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+}
+
+// Place this CTA's choices: cnt[warp][g] holds the warp's next slot of expert g.
+template <typename ID>
+MX_DEVICE_INLINE void route_place(const RouteParams &p, int64_t begin, int64_t end, int64_t per_warp, int *cnt) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t w0 = begin + warp * per_warp, w1 = min(w0 + per_warp, end);
+    for (int64_t i = w0; i < w1; i += 32) {
+        const int g = route_id<ID>(p, i + lane, w1);
+        const uint32_t same = __match_any_sync(0xffffffffu, g);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        int at = -1;
+        if (g >= 0) at = cnt[warp * p.groups + g] + rank;
+        __syncwarp();
+        if (g >= 0 && (__ffs(same) - 1) == lane) cnt[warp * p.groups + g] += __popc(same);
+        __syncwarp();
+        if (i + lane < w1) {
+            p.slot[i + lane] = at;
+            if (at >= 0) p.row_token[at] = (int32_t)((i + lane) / p.choices);
+        }
+    }
+}
+
+// Rows behind the last slot belong to no token.
+MX_DEVICE_INLINE void route_fill_tail(const RouteParams &p, int64_t live, int64_t begin, int64_t end) {
+    for (int64_t i = max(live, begin) + threadIdx.x; i < end; i += kRouteThreads) p.row_token[i] = -1;
+}
+
+// All of it in one CTA (n <= kRouteChunk).  Dynamic shared memory: 32 x groups ints.
+template <typename ID>
+__global__ void __launch_bounds__(kRouteThreads) route_small_kernel(RouteParams p) {
+    extern __shared__ int cnt[];
+    __shared__ int warp_sums[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t per_warp = ((p.n + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32;
+    route_count<ID>(p, 0, p.n, per_warp, cnt);
+    const int g = threadIdx.x;   // groups <= kRouteThreads
+    int sum = 0;
+    if (g < p.groups)
+        for (int w = 0; w < kRouteWarps; ++w) sum += cnt[w * p.groups + g];
+    int total;
+    int base = block_exclusive(sum, warp_sums, total);
+    if (g < p.groups) {
+        p.offsets[g] = base;
+        for (int w = 0; w < kRouteWarps; ++w) {
+            const int c = cnt[w * p.groups + g];
+            cnt[w * p.groups + g] = base;
+            base += c;
+        }
+    }
+    if (threadIdx.x == 0) p.offsets[p.groups] = total;
+    __syncthreads();
+    route_place<ID>(p, 0, p.n, per_warp, cnt);
+    route_fill_tail(p, total, 0, p.n);
+}
+
+// Larger n: counts per chunk, one prefix sum over [groups][chunks], placing.
+template <typename ID>
+__global__ void __launch_bounds__(kRouteThreads) route_count_kernel(RouteParams p) {
+    extern __shared__ int cnt[];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t begin = (int64_t)blockIdx.x * kRouteChunk, end = min(begin + kRouteChunk, p.n);
+    route_count<ID>(p, begin, end, kRouteChunk / kRouteWarps, cnt);
+    for (int g = threadIdx.x; g < p.groups; g += kRouteThreads) {
+        int sum = 0;
+        for (int w = 0; w < kRouteWarps; ++w) sum += cnt[w * p.groups + g];
+        p.counts[(int64_t)g * p.chunks + blockIdx.x] = sum;
+    }
+}
+
+static __global__ void __launch_bounds__(kRouteThreads) route_scan_kernel(RouteParams p) {
+    __shared__ int warp_sums[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t m = (int64_t)p.groups * p.chunks;
+    const int64_t per = (m + kRouteThreads - 1) / kRouteThreads;
+    const int64_t i0 = min((int64_t)threadIdx.x * per, m), i1 = min(i0 + per, m);
+    int sum = 0;
+    for (int64_t i = i0; i < i1; ++i) sum += p.counts[i];
+    int total;
+    int base = block_exclusive(sum, warp_sums, total);
+    for (int64_t i = i0; i < i1; ++i) {
+        const int c = p.counts[i];
+        p.counts[i] = base;
+        if (i % p.chunks == 0) p.offsets[i / p.chunks] = base;
+        base += c;
+    }
+    if (threadIdx.x == 0) p.offsets[p.groups] = total;
+}
+
+template <typename ID>
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(RouteParams p) {
+    extern __shared__ int cnt[];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t begin = (int64_t)blockIdx.x * kRouteChunk, end = min(begin + kRouteChunk, p.n);
+    route_count<ID>(p, begin, end, kRouteChunk / kRouteWarps, cnt);
+    for (int g = threadIdx.x; g < p.groups; g += kRouteThreads) {
+        int base = p.counts[(int64_t)g * p.chunks + blockIdx.x];
+        for (int w = 0; w < kRouteWarps; ++w) {
+            const int c = cnt[w * p.groups + g];
+            cnt[w * p.groups + g] = base;
+            base += c;
+        }
+    }
+    __syncthreads();
+    route_place<ID>(p, begin, end, kRouteChunk / kRouteWarps, cnt);
+    route_fill_tail(p, p.offsets[p.groups], begin, end);
+}
+
+struct CombineParams {
+    const uint16_t *y;        // [rows][ldy]
+    int64_t ldy;
+    int64_t rows;
+    const int32_t *slot;      // [tokens][choices]
+    const float *weights;     // [tokens][choices]
+    int choices;
+    int64_t cols;
+    uint16_t *out;            // [tokens][ldo]
+    int64_t ldo;
+};
+
+// One thread: VEC columns of one token, the choices eight loads at a time.
+template <int VEC>
+__global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
+    const int64_t t = blockIdx.x;
+    const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * VEC;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (c >= p.cols) return;
+    float acc[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
+    for (int j0 = 0; j0 < p.choices; j0 += 8) {
+        uint4 v[8];
+        float w[8];
+        bool on[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            on[j] = false;
+            if (j0 + j < p.choices) {
+                const int64_t s = __ldg(p.slot + t * p.choices + j0 + j);
+                on[j] = s >= 0 && s < p.rows;
+                w[j] = __ldg(p.weights + t * p.choices + j0 + j);
+                if (on[j]) {
+                    if (VEC == 8) v[j] = ldg_stream(p.y + s * p.ldy + c);
+                    else v[j].x = p.y[s * p.ldy + c];
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!on[j]) continue;
+            const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                acc[e] = __fmaf_rn(w[j], (e & 1) ? bf16hi(u[e >> 1]) : bf16lo(u[e >> 1]), acc[e]);
+        }
+    }
+    if (VEC == 8) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(acc[(2 * e) % VEC], acc[(2 * e + 1) % VEC]);
+            o[e] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p.out + t * p.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+        p.out[t * p.ldo + c] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
+    }
+}
+
+}  // namespace mx

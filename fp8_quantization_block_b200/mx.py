@@ -22,7 +22,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmx.so")
 
 MX_MXFP8_E4M3, MX_MXFP8_E5M2, MX_MXFP4, MX_NVFP4, MX_MXFP6_E3M2, MX_MXFP4_MBS = 0, 1, 2, 3, 4, 5
-FORMATS = {"mxfp8_e4m3": 0, "mxfp8_e5m2": 1, "mxfp4": 2, "nvfp4": 3, "mxfp6_e3m2": 4, "mxfp4_mbs": 5}
+MX_FP8_B128, MX_FP8_B128X128 = 6, 8
+FORMATS = {"mxfp8_e4m3": 0, "mxfp8_e5m2": 1, "mxfp4": 2, "nvfp4": 3, "mxfp6_e3m2": 4, "mxfp4_mbs": 5,
+           "fp8_b128": 6, "fp8_b128x128": 8}
 MX_OK, MX_ERR_INVALID_ARG, MX_ERR_UNSUPPORTED_SHAPE, MX_ERR_MISALIGNED = 0, 1, 2, 3
 MX_ERR_CUDA, MX_ERR_TIMEOUT, MX_ERR_DEVICE = 4, 5, 6
 MX_EPI_NONE, MX_EPI_GELU = 0, 1
@@ -39,7 +41,10 @@ EXPORTED = [
     "mx_gemm_fused_act", "mx_fused_workspace_bytes", "mx_check_device_error", "mx_status_string",
     "mx_version", "mx_debug_set", "mx_gemm_fused_act_noalloc", "mx_quantize_oas", "mx_qsnr",
     "mx_quantize_rht", "mx_quantize_mbs_dynamic", "mx_fused_split_workspace_bytes", "mx_debug_split_units",
+    "mx_route_workspace_bytes", "mx_route", "mx_grouped_scales_bytes", "mx_quantize_grouped", "mx_gemm_grouped",
+    "mx_combine",
 ]
+MX_MAX_GROUPS = 1024
 MX_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -55,6 +60,10 @@ class MxTensorC(ctypes.Structure):
                 ("gscale", ctypes.c_void_p)]
 
 
+class MxGroupsC(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("reserved", ctypes.c_int32), ("offsets", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -68,6 +77,7 @@ def lib() -> ctypes.CDLL:
             L = ctypes.CDLL(LIB_PATH)
             P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
             T = ctypes.POINTER(MxTensorC)
+            G = ctypes.POINTER(MxGroupsC)
             sigs = {
                 "mx_codes_bytes": (sz, [i32, i64, i64]),
                 "mx_scales_bytes": (sz, [i32, i64, i64]),
@@ -88,6 +98,12 @@ def lib() -> ctypes.CDLL:
                 "mx_status_string": (ctypes.c_char_p, [i32]),
                 "mx_version": (i32, []),
                 "mx_debug_set": (i32, [i32, ctypes.c_uint64]),
+                "mx_route_workspace_bytes": (sz, [i64, i32, i32]),
+                "mx_route": (i32, [P, i32, i64, i32, i32, P, P, P, P, sz, P]),
+                "mx_grouped_scales_bytes": (sz, [i32, i64, i64, i64]),
+                "mx_quantize_grouped": (i32, [i32, P, i64, i64, i64, P, G, T, P, P]),
+                "mx_gemm_grouped": (i32, [T, T, G, P, i64, i32, P]),
+                "mx_combine": (i32, [P, i64, i64, i64, P, P, i64, i32, P, i64, P]),
             }
             for name, (res, args) in sigs.items():
                 f = getattr(L, name)
@@ -169,6 +185,35 @@ def split_units(tiles: int, workers: int, kt: int, mode: int, worker: int):
     buf = (ctypes.c_int32 * (5 * max(n, 1)))()
     lib().mx_debug_split_units(tiles, workers, kt, mode, worker, buf, n, None)
     return n_workers.value, [tuple(buf[5 * u:5 * u + 5]) for u in range(n)]
+
+
+def mx_route_workspace_bytes(tokens: int, choices: int, groups: int) -> int:
+    return int(lib().mx_route_workspace_bytes(tokens, choices, groups))
+
+
+def mx_route(ids_ptr, id_bits, tokens, choices, groups, offsets_ptr, row_token_ptr, slot_ptr, ws_ptr, ws_bytes,
+             stream) -> int:
+    return int(lib().mx_route(ids_ptr, id_bits, tokens, choices, groups, offsets_ptr, row_token_ptr, slot_ptr, ws_ptr,
+                              ws_bytes, stream))
+
+
+def mx_grouped_scales_bytes(fmt: int, rows: int, groups: int, cols: int) -> int:
+    return int(lib().mx_grouped_scales_bytes(fmt, rows, groups, cols))
+
+
+def mx_quantize_grouped(fmt, src_ptr, src_rows, K, ld, row_index_ptr, groups: MxGroupsC, dst: MxTensorC, gscale_in_ptr,
+                        stream) -> int:
+    return int(lib().mx_quantize_grouped(fmt, src_ptr, src_rows, K, ld, row_index_ptr, ctypes.byref(groups),
+                                         ctypes.byref(dst), gscale_in_ptr, stream))
+
+
+def mx_gemm_grouped(A: MxTensorC, B: MxTensorC, groups: MxGroupsC, C_ptr, ldc, epilogue, stream) -> int:
+    return int(lib().mx_gemm_grouped(ctypes.byref(A), ctypes.byref(B), ctypes.byref(groups), C_ptr, ldc, epilogue,
+                                     stream))
+
+
+def mx_combine(Y_ptr, rows, cols, ldy, slot_ptr, weights_ptr, tokens, choices, out_ptr, ldo, stream) -> int:
+    return int(lib().mx_combine(Y_ptr, rows, cols, ldy, slot_ptr, weights_ptr, tokens, choices, out_ptr, ldo, stream))
 
 
 def mx_check_device_error(stream=None):
@@ -315,6 +360,192 @@ def fused_workspace(fmt: int, M: int, K: int, device="cuda", split: bool = True)
     blocks); split: with room for the K split of the last wave."""
     n = mx_fused_split_workspace_bytes(fmt, M, K) if split else mx_fused_workspace_bytes(fmt, M, K)
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+# ----------------------------------------------------------------- mixture of experts
+@dataclass
+class Routing:
+    """What mx_route writes: groups of slots, and slots from and to the tokens' choices."""
+    offsets: torch.Tensor     # int32 [experts + 1]
+    row_token: torch.Tensor   # int32 [tokens * choices]: the token of each slot, -1 behind the last
+    slot: torch.Tensor        # int32 [tokens, choices]: the slot of each choice, -1 where it has none
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows_ok(x: torch.Tensor, what: str) -> None:
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] <= 1),
+          f"{what}: a bf16 matrix with contiguous rows is wanted")
+
+
+def _pitch(x: torch.Tensor) -> int:
+    """Row pitch of a matrix (a single row's stride says nothing)."""
+    return x.stride(0) if x.shape[0] > 1 else max(x.shape[1], x.stride(0) // 8 * 8)
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    for t in others:
+        _need(t is None or t.device == first.device, "all tensors on one device are wanted")
+
+
+class _On:
+    """The device of a call's tensors made current around it, where it is another than the current one."""
+    __slots__ = ("back", "stream")
+
+    def __init__(self, t: torch.Tensor, stream):
+        _need(t.is_cuda, "CUDA tensors are wanted")
+        dev, now = t.device.index, torch.cuda.current_device()
+        self.back = now if now != dev else -1
+        if self.back >= 0:
+            torch.cuda.set_device(dev)
+        self.stream = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+    def __enter__(self):
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.back >= 0:
+            torch.cuda.set_device(self.back)
+
+
+def _groups(offsets: torch.Tensor) -> MxGroupsC:
+    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous() and offsets.numel() >= 2,
+          "offsets: a contiguous int32 vector of groups + 1 is wanted")
+    return MxGroupsC(offsets.numel() - 1, 0, offsets.data_ptr())
+
+
+def route(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = None, stream=None) -> Routing:
+    """Expert ids [tokens, choices] (int32 or int64; others than 0 .. experts - 1 have no slot) -> Routing."""
+    _need(ids.dtype in (torch.int32, torch.int64) and ids.dim() == 2 and ids.is_contiguous(),
+          "ids: a contiguous int32 or int64 matrix is wanted")
+    tokens, choices = ids.shape
+    n, dev = tokens * choices, ids.device
+    with _On(ids, stream) as st:
+        both = torch.empty(experts + 1 + 2 * n, dtype=torch.int32, device=dev)
+        r = Routing(both[:experts + 1], both[experts + 1:experts + 1 + n], both[experts + 1 + n:].view(tokens, choices))
+        need = mx_route_workspace_bytes(tokens, choices, experts)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _same_device(ids, workspace)
+        at = both.data_ptr()
+        check(mx_route(ids.data_ptr(), 32 if ids.dtype == torch.int32 else 64, tokens, choices, experts, at,
+                       at + 4 * (experts + 1), at + 4 * (experts + 1 + n), _ptr(workspace),
+                       0 if workspace is None else workspace.numel() * workspace.element_size(), st), "mx_route")
+    return r
+
+
+def empty_grouped(fmt: int, rows: int, groups: int, cols: int, device="cuda") -> MxTensor:
+    """Buffers of a grouped activation (the scales of mx_quantize_grouped)."""
+    codes = torch.empty(max(mx_codes_bytes(fmt, rows, cols), 1), dtype=torch.uint8, device=device)
+    scales = torch.empty(max(mx_grouped_scales_bytes(fmt, rows, groups, cols), 1), dtype=torch.uint8, device=device)
+    g = torch.empty(1, dtype=torch.float32, device=device) if fmt == MX_NVFP4 else None
+    return MxTensor(fmt, rows, cols, codes, scales, g)
+
+
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
+def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, row_index: torch.Tensor | None = None,
+                     gscale: torch.Tensor | None = None, out: MxTensor | None = None, stream=None) -> MxTensor:
+    """Rows of x (x[row_index[t]], or x itself) quantized for gemm_grouped.  NVFP4 wants gscale (g)."""
+    _rows_ok(x, "x")
+    groups = _groups(offsets)
+    K = x.shape[1]
+    if row_index is not None:
+        _need(row_index.dtype == torch.int32 and row_index.dim() == 1 and row_index.is_contiguous(),
+              "row_index: a contiguous int32 vector is wanted")
+    rows = x.shape[0] if row_index is None else row_index.numel()
+    if out is None:
+        out = empty_grouped(fmt, rows, groups.count, K, x.device)
+    else:
+        _need(out.fmt == fmt and out.rows == rows and out.cols == K, "out: another format or size")
+        _need(_nbytes(out.codes) >= mx_codes_bytes(fmt, rows, K) and
+              _nbytes(out.scales) >= mx_grouped_scales_bytes(fmt, rows, groups.count, K), "out: a buffer is too small")
+    _same_device(x, offsets, row_index, gscale, out.codes, out.scales, out.gscale)
+    with _On(x, stream) as st:
+        check(mx_quantize_grouped(fmt, x.data_ptr(), x.shape[0], K, _pitch(x), _ptr(row_index), groups, out.c(),
+                                  _ptr(gscale), st), "mx_quantize_grouped")
+    return out
+
+
+def quantize_experts(w: torch.Tensor, fmt: int, stream=None) -> MxTensor:
+    """bf16 [experts, N, K] -> the experts' matrices one after another, as gemm_grouped takes them for B (rows N)."""
+    _need(w.dtype == torch.bfloat16 and w.dim() == 3 and w.stride(2) == 1, "w: bf16 [experts, N, K] is wanted")
+    E, N, K = w.shape
+    cb, sb = mx_codes_bytes(fmt, N, K), mx_scales_bytes(fmt, N, K)
+    codes = torch.empty(max(E * cb, 1), dtype=torch.uint8, device=w.device)
+    scales = torch.empty(max(E * sb, 1), dtype=torch.uint8, device=w.device)
+    g = torch.empty(E, dtype=torch.float32, device=w.device) if fmt == MX_NVFP4 else None
+    with _On(w, stream) as st:
+        for e in range(E):
+            one = MxTensorC(fmt, 0, N, K, codes.data_ptr() + e * cb, scales.data_ptr() + e * sb,
+                            None if g is None else g.data_ptr() + 4 * e)
+            check(mx_quantize(fmt, w[e].data_ptr(), N, K, _pitch(w[e]), one, None, st), "mx_quantize")
+    return MxTensor(fmt, N, K, codes, scales, g)
+
+
+def gemm_grouped(A: MxTensor, B: MxTensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
+                 epilogue: int = MX_EPI_NONE, stream=None) -> torch.Tensor:
+    """C[t] = f(A[t] B_g^T) for the rows t of every group g; B as quantize_experts gives it.  bf16 [A.rows, B.rows],
+    rows of no group left as they are."""
+    groups = _groups(offsets)
+    E = groups.count
+    _need(_nbytes(A.codes) >= mx_codes_bytes(A.fmt, A.rows, A.cols) and
+          _nbytes(A.scales) >= mx_grouped_scales_bytes(A.fmt, A.rows, E, A.cols), "A: a buffer is too small")
+    _need(_nbytes(B.codes) >= E * mx_codes_bytes(B.fmt, B.rows, B.cols) and
+          _nbytes(B.scales) >= E * mx_scales_bytes(B.fmt, B.rows, B.cols) and
+          (B.gscale is None or B.gscale.numel() >= E), "B: fewer matrices than groups")
+    if out is None:
+        out = torch.empty((A.rows, B.rows), dtype=torch.bfloat16, device=A.codes.device)
+    else:
+        _rows_ok(out, "out")
+        _need(out.shape == (A.rows, B.rows), "out: another size")
+    _same_device(A.codes, A.scales, A.gscale, B.codes, B.scales, B.gscale, offsets, out)
+    with _On(A.codes, stream) as st:
+        check(mx_gemm_grouped(A.c(), B.c(), groups, out.data_ptr(), max(out.stride(0), B.rows) if A.rows == 1 else out.stride(0),
+                              epilogue, st), "mx_gemm_grouped")
+    return out
+
+
+def combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, out: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] y[slot[t, j]] over the slots inside y: bf16 [tokens, y.shape[1]]."""
+    _rows_ok(y, "y")
+    _need(slot.dtype == torch.int32 and slot.dim() == 2 and slot.is_contiguous(), "slot: a contiguous int32 matrix is wanted")
+    _need(weights.dtype == torch.float32 and weights.shape == slot.shape and weights.is_contiguous(),
+          "weights: a contiguous float32 matrix of slot's shape is wanted")
+    tokens, choices = slot.shape
+    if out is None:
+        out = torch.empty((tokens, y.shape[1]), dtype=torch.bfloat16, device=y.device)
+    else:
+        _rows_ok(out, "out")
+        _need(out.shape == (tokens, y.shape[1]), "out: another size")
+    _same_device(y, slot, weights, out)
+    with _On(y, stream) as st:
+        check(mx_combine(y.data_ptr(), y.shape[0], y.shape[1], max(y.stride(0), y.shape[1]), slot.data_ptr(),
+                         weights.data_ptr(), tokens, choices, out.data_ptr(), max(out.stride(0), y.shape[1]), st),
+              "mx_combine")
+    return out
+
+
+def experts_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W1: MxTensor, W2: MxTensor,
+                x_gscale: torch.Tensor | None = None, h_gscale: torch.Tensor | None = None,
+                act_fmt: int | None = None, stream=None) -> torch.Tensor:
+    """A mixture of experts' MLP: out[t] = sum_j weights[t, j] W2_e GELU(W1_e x[t]), e = ids[t, j].
+
+    W1 [experts x N x K] and W2 [experts x K' x N] as quantize_experts gives them; activations are quantized to
+    act_fmt (default: the format that goes with the weights').  NVFP4 wants the activations' g (x_gscale, h_gscale)."""
+    fmt = act_fmt if act_fmt is not None else (MX_FP8_B128 if W1.fmt == MX_FP8_B128X128 else W1.fmt)
+    experts = W1.codes.numel() // max(mx_codes_bytes(W1.fmt, W1.rows, W1.cols), 1)
+    r = route(ids, experts, stream=stream)
+    h = gemm_grouped(quantize_grouped(x, r.offsets, fmt, row_index=r.row_token, gscale=x_gscale, stream=stream), W1,
+                     r.offsets, epilogue=MX_EPI_GELU, stream=stream)
+    y = gemm_grouped(quantize_grouped(h, r.offsets, fmt, gscale=h_gscale, stream=stream), W2, r.offsets, stream=stream)
+    return combine(y, r.slot, weights, stream=stream)
 
 
 def check_device_error(stream=None) -> None:

@@ -54,14 +54,20 @@ extern "C" {
  * with the base-block scales, and the macro factors are applied to that
  * partial sum on the CUDA cores.
  * E3M2 ([MX] format table, MXFP6): sign, 3 exponent bits with bias 3, 2
- * mantissa bits, no infinities or NaN, largest magnitude 28. */
+ * mantissa bits, no infinities or NaN, largest magnitude 28.
+ * FP8_B128 and FP8_B128X128: E4M3 with one FP32 scale s per block of 1 x 128
+ * (activations) or 128 x 128 (weights), the usual form of FP8 weights of large
+ * language models; a pair of formats for one product, A in the first and B in
+ * the second.  (The value 7 is no format.) */
 typedef enum {
     MX_MXFP8_E4M3 = 0,
     MX_MXFP8_E5M2 = 1,
     MX_MXFP4 = 2,
     MX_NVFP4 = 3,
     MX_MXFP6_E3M2 = 4,
-    MX_MXFP4_MBS = 5
+    MX_MXFP4_MBS = 5,
+    MX_FP8_B128 = 6,
+    MX_FP8_B128X128 = 8
 } mx_format;
 
 typedef enum {
@@ -89,6 +95,10 @@ typedef enum {
  *           Padding bytes (rows >= rows, columns >= C) are 0.  MXFP4_MBS
  *           appends its macro bytes, [rows][cols/128] row-major, zero-padded to
  *           a multiple of 16 bytes, after the tiles.
+ *           FP8_B128: FP32, scale (r, b) of row r and K block b at float b *
+ *           P + r with P = rows rounded up to a multiple of 4 (padding 0).
+ *           FP8_B128X128: FP32, scale (r / 128, b) at float (r / 128) *
+ *           (cols / 128) + b, the buffer rounded up to 16 bytes.
  *   gscale: device, one float (NVFP4 only; NULL otherwise): the per-tensor
  *           decode multiplier g.  Real value = g * scale * element.           */
 typedef struct {
@@ -104,7 +114,8 @@ typedef struct {
 /* Sizes in bytes of the two buffers of an mx_tensor.  0 for a bad format. */
 size_t mx_codes_bytes(int fmt, int64_t rows, int64_t cols);
 size_t mx_scales_bytes(int fmt, int64_t rows, int64_t cols);
-/* Elements per scale block: 32 (MX formats) or 16 (NVFP4); 0 for a bad format. */
+/* Elements per scale block along K: 32 (MX formats), 16 (NVFP4) or 128 (the
+ * FP8 block formats); 0 for a bad format. */
 int mx_block_size(int fmt);
 
 /* Quantize a bf16 matrix src [M x K] (row pitch ld_src elements, ld_src >= K,
@@ -125,6 +136,9 @@ int mx_block_size(int fmt);
  *     zero block); per 16 elements E = the smallest exponent with max|x| <=
  *     6 (1 + m/256) 2^(E-127); elements = RNE of the exact quotient
  *     x / ((1 + m/256) 2^(E-127)) onto E2M1, saturating at 6.  K % 128 == 0.
+ *   FP8_B128, FP8_B128X128: per block s = RN_fp32(max|x| / 448); elements =
+ *     RNE of the exact quotient x / s onto E4M3, saturating at 448 (a block of
+ *     zeros: s = 0 and the zeros themselves).  K % 128 == 0.
  * Rounding is to nearest, ties to even; a value that rounds to zero keeps its
  * sign.  K must be a multiple of the block size (32, or 16 for NVFP4).
  * dst->rows/cols must equal M/K and dst->fmt must equal fmt.  Non-finite
@@ -198,7 +212,10 @@ mx_status mx_qsnr(const mx_tensor *q, const void *src_bf16, int64_t ld_src, doub
  * all with E8M0 scales on 32-element blocks), which run on kind::mxf8f6f4 at
  * the FP8 rate (MXFP6 x MXFP6 included); such a call needs the codes of an
  * FP6 or FP4 operand 32-byte aligned (else MX_ERR_MISALIGNED).  NVFP4 pairs
- * only with NVFP4.  C is bf16 [M x N] with row pitch ldc (ldc >= N).  Accuracy contract:
+ * only with NVFP4, and FP8_B128 (A) only with FP8_B128X128 (B): there the
+ * tensor core sums each block's products in FP32, and the CUDA cores add them
+ * up times the two scales, in FP32.  C is bf16 [M x N] with row pitch ldc
+ * (ldc >= N).  Accuracy contract:
  *   |C - C_ref| <= 2^-8 |C_ref| + 1e-4 (|A_dq| |B_dq|^T)  elementwise.       */
 mx_status mx_gemm(const mx_tensor *A, const mx_tensor *B, void *C_bf16, int64_t ldc, void *stream);
 
@@ -255,6 +272,8 @@ typedef enum { MX_EPI_NONE = 0, MX_EPI_GELU = 1 } mx_epilogue;
  *     x_amax   : device float holding amax(|X|); g = RU_fp32(amax / 2688);
  *     neither  : amax(|X|) is computed on the device: by a pre-pass over X,
  *                or, for M*K <= 16384, by every CTA of the quantize kernel.
+ * FP8_B128 (W in FP8_B128X128) runs as the quantize and then the GEMM, in
+ * stream order, and takes no amax_out.
  * K % 128 == 0, ldx % 8 == 0. */
 mx_status mx_gemm_fused_act(int fmt, const void *X_bf16, int64_t M, int64_t K, int64_t ldx,
                             const mx_tensor *W, void *C_bf16, int64_t ldc, int epilogue,
@@ -298,6 +317,74 @@ mx_status mx_gemm_fused_act_noalloc(int fmt, const void *X_bf16, int64_t M, int6
                                     const mx_tensor *W, void *C_bf16, int64_t ldc, int epilogue,
                                     float *amax_out, const float *x_gscale, const float *x_amax,
                                     void *stream);
+
+/* ---- Mixture of experts: rows grouped by expert --------------------------
+ * Group g has the rows [offsets[g], offsets[g + 1]) of a matrix whose groups
+ * follow one another; offsets is a device array of count + 1 ascending int32
+ * that starts at 0 (the host never reads it, so a call can follow the one that
+ * writes it).  Groups may be empty.  Rows from offsets[count] on belong to no
+ * group: no call reads or writes them (an output's rows there are left as they
+ * are).  Offsets outside [0, rows] are clipped to it. */
+typedef struct {
+    int32_t count;
+    int32_t reserved;
+    const int32_t *offsets;
+} mx_groups;
+#define MX_MAX_GROUPS 1024
+
+/* From the experts chosen for each token to slots.  ids: device, [tokens x
+ * choices] int32 or int64 (id_bits 32 or 64).  The slot of a choice is its
+ * place among all choices sorted by expert, stably (by token, then choice):
+ *   offsets   [groups + 1] the groups of the slots;
+ *   row_token [tokens * choices] the token of each slot, -1 for slots from
+ *             offsets[groups] on;
+ *   slot      [tokens * choices] the slot of each choice, -1 for an id outside
+ *             [0, groups) (a padded or dropped choice).
+ * The same expert twice in a token gives two slots.  workspace: device, 4-byte
+ * aligned, mx_route_workspace_bytes bytes (0 for up to 8192 choices: NULL will
+ * do); scratch, not to be shared by calls that overlap on the GPU.
+ * groups <= MX_MAX_GROUPS, tokens * choices < 2^31. */
+size_t mx_route_workspace_bytes(int64_t tokens, int choices, int groups);
+mx_status mx_route(const void *ids, int id_bits, int64_t tokens, int choices, int groups, int32_t *offsets,
+                   int32_t *row_token, int32_t *slot, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Quantize rows gathered into groups: row t of dst (t < offsets[count]) is
+ * row row_index[t] of src [src_rows x K] (row t where row_index is NULL),
+ * quantized as mx_quantize does; a row whose index lies outside [0, src_rows)
+ * is a row of zeros.  dst->rows is the number of rows T; its codes are as
+ * mx_quantize's, its scales, of mx_grouped_scales_bytes bytes, as follows:
+ *   FP8_B128: as mx_quantize's (of rows >= offsets[count]: left as they are);
+ *   the other formats: each group begins a 128-row band of scale tiles, so row
+ *   r of group g is row 128 * (sum of ceil(rows / 128) over the groups before
+ *   g) + r of the tiled layout; all other bytes are 0.
+ * NVFP4: gscale_in (not NULL) is the device float g.  Formats: all that
+ * mx_gemm_grouped takes for A.  T < 2^31. */
+size_t mx_grouped_scales_bytes(int fmt, int64_t rows, int64_t groups, int64_t cols);
+mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, int64_t K, int64_t ld_src,
+                              const int32_t *row_index, const mx_groups *groups, mx_tensor *dst,
+                              const float *gscale_in, void *stream);
+
+/* The experts' products:
+ *   C[t][j] = RNE_bf16(f(sum_k A_dq[t][k] * B_g,dq[j][k]))  for every row t of group g,
+ * A [T x K] as mx_quantize_grouped writes it, C bf16 [T x N] with pitch ldc,
+ * f the identity or GELU (mx_epilogue).  B describes one group's matrix (rows
+ * = N, cols = K); its buffers hold the groups' matrices one after another:
+ * codes mx_codes_bytes(B->fmt, N, K) apart, scales mx_scales_bytes(B->fmt, N,
+ * K) apart, NVFP4 gscale one float apart.  Formats as for mx_gemm, without
+ * MXFP4_MBS; in a product of two MX formats that differ (or of E5M2 or E3M2)
+ * the codes of an FP6 or FP4 operand are 32-byte aligned.  K % 128 == 0,
+ * K > 0.  Accuracy contract as mx_gemm's. */
+mx_status mx_gemm_grouped(const mx_tensor *A, const mx_tensor *B, const mx_groups *groups, void *C_bf16, int64_t ldc,
+                          int epilogue, void *stream);
+
+/* The tokens' results from the experts' rows:
+ *   out[t][c] = RNE_bf16(sum_j weights[t][j] * Y[slot[t][j]][c]),
+ * summed in FP32, j ascending, over the choices whose slot lies in [0, rows)
+ * (0 where none does).  Y bf16 [rows x cols] (pitch ldy), slot and weights
+ * [tokens x choices], out bf16 [tokens x cols] (pitch ldo); no alignment
+ * beyond the elements' own is needed (16-byte rows run faster). */
+mx_status mx_combine(const void *Y_bf16, int64_t rows, int64_t cols, int64_t ldy, const int32_t *slot,
+                     const float *weights, int64_t tokens, int choices, void *out_bf16, int64_t ldo, void *stream);
 
 /* Synchronize `stream`, then read and clear the device error word.  Returns
  * MX_OK, MX_ERR_TIMEOUT (a bounded wait inside a kernel gave up: the kernel
