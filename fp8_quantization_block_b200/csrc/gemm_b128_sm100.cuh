@@ -17,6 +17,12 @@
 //   warp 1       TMEM owner and MMA issuer: 4 MMAs of K = 32 per stage into one
 //                of the partial buffers (2 of 256 columns, or 4 of 128), which
 //                then holds that block's P_b alone;
+//   warps 2-3    scales: the rows' sA and the tile's (at most three) sB of each
+//                block, copied asynchronously into a ring in shared memory up to
+//                16 blocks ahead (their latency beside a saturated weight
+//                stream is several blocks' time).  The drain warps carry no
+//                global loads: an arrive on a barrier would wait for any load
+//                still in flight;
 //   warps 4-11   two per TMEM lane quadrant: drain a partial buffer (half of
 //                its columns each) while the next block's MMAs run, then
 //                [GELU], bf16 and store after the last block.
@@ -38,10 +44,11 @@ namespace mx {
 constexpr int kB128Threads = 384;
 constexpr int kB128DrainWarps = 8;
 constexpr int kB128MaxStages = 16;
-constexpr int kB128StagingBytes = kB128DrainWarps * 2 * kEpiChunkBytes;   // two 32 x 32 bf16 buffers per drain warp
-// registers per thread: the sum over the three warpgroups is what the block
-// is launched with (384 threads at 168)
-constexpr int kB128DrainRegs = 216, kB128OtherRegs = 72;
+// Registers per thread; the sum over the three warpgroups is what the block is
+// launched with (384 threads at 168).  Measured on 8192^3: 200 for the drain
+// warps 644 us, 216 740 us (the scheduler then overlaps more loads and spills
+// instead), 176 688 us.
+constexpr int kB128DrainRegs = 200, kB128OtherRegs = 104;
 static_assert(2 * kB128DrainRegs + kB128OtherRegs <= 3 * 168, "register split");
 
 struct B128GemmParams {
@@ -58,12 +65,20 @@ struct B128GemmParams {
     int m_blocks, n_blocks;
     int stages;
     int a_bytes, b_bytes;  // per stage and CTA
+    int staging_bytes;     // kB128StagingBytes where vec_store is 0
     int epilogue;          // 0 none, 1 GELU
-    int use_tma_store;     // C 16-byte aligned, ldc % 8 == 0
+    int vec_store;         // 2: every row of C starts on 32 bytes, 1: on 16 bytes, 0: neither
     int skip_producer;
     uint64_t wait_limit_ns;
     Groups groups;         // GROUPED
 };
+
+constexpr int kB128ScaleGroup = 4;     // blocks per barrier of the scale ring
+constexpr int kB128ScaleGroups = 4;
+constexpr int kB128ScaleSlots = kB128ScaleGroup * kB128ScaleGroups;
+constexpr int kB128SlotFloats = 132;   // 128 rows, 3 column blocks
+// shared memory beside the stage ring and the staging rows
+constexpr int kB128FixedBytes = 1024 + kB128ScaleSlots * kB128SlotFloats * 4 + (2 * kB128MaxStages + 8 + 2 * kB128ScaleGroups + 1) * 8 + 16;
 
 // Instruction descriptor of kind::f8f6f4: FP32 accumulator, E4M3 x E4M3, both K-major.
 MX_DEVICE_INLINE uint32_t b128_idesc(int m, int n) {
@@ -115,63 +130,73 @@ class B128Tiles<false> {
     const B128GemmParams &p_;
 };
 
-// One 32-column chunk (rows m0q + lane, columns col ..) of C through this
-// warp's staging buffers: a TMA store where all 32 rows are the tile's own (a
-// store clips at the matrix's edges, not at a group's), else row by row, each
-// row's columns as one coalesced write.
-MX_DEVICE_INLINE void b128_store_chunk(const B128GemmParams &p, const CUtensorMap *tmC, const uint32_t (&packed)[16],
-                                       int m0q, int row_end, int col, int lane, uint8_t *bufs, uint32_t &nstore) {
-    uint8_t *buf = bufs + (nstore & 1u) * kEpiChunkBytes;
-    ++nstore;
-    if (lane == 0) bulk_wait_group_read<1>();   // this buffer's previous store has read it
-    __syncwarp();
-    uint4 *dst = reinterpret_cast<uint4 *>(buf + lane * 64);
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-        dst[v] = make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
-    if (p.use_tma_store && (m0q + 32 <= row_end || row_end == p.M)) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(tmC, col, m0q, buf);
-            bulk_commit_group();
+// bf16 pairs of 16 columns of this lane's row, to C.
+MX_DEVICE_INLINE void b128_store_row16(const B128GemmParams &p, const uint32_t (&h)[8], int row, int col) {
+    uint16_t *dst = p.C + (int64_t)row * p.ldc + col;
+    if (col + 16 <= p.N) {
+        if (p.vec_store == 2) {
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                         "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                         : "memory");
+        } else {
+            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(h[4], h[5], h[6], h[7]);
         }
     } else {
-        __syncwarp();
-        const int rows = min(32, row_end - m0q), cols = min(32, p.N - col);
-        uint16_t *c = p.C + (int64_t)m0q * p.ldc + col;
-        if (p.use_tma_store && cols == 32) {
-            // eight rows at a time, 16 bytes per lane
-            for (int r = lane >> 2; r < rows; r += 8)
-                *reinterpret_cast<uint4 *>(c + (int64_t)r * p.ldc + 8 * (lane & 3)) =
-                    *reinterpret_cast<const uint4 *>(buf + r * 64 + 16 * (lane & 3));
-        } else {
-            for (int r = 0; r < rows; ++r)
-                if (lane < cols) c[(int64_t)r * p.ldc + lane] = *reinterpret_cast<const uint16_t *>(buf + r * 64 + 2 * lane);
-        }
-        __syncwarp();
-        if (lane == 0) bulk_commit_group();   // an empty group keeps the buffers' order of groups
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (col + e < p.N) dst[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
     }
 }
 
+// The same for rows that start off a 16-byte boundary (an odd width or pitch):
+// through shared memory (kB128StagePitch words per row), two rows of 16 columns
+// per store of the warp.
+constexpr int kB128StagePitch = 9;
+constexpr int kB128StagingBytes = kB128DrainWarps * 32 * kB128StagePitch * 4;
+MX_DEVICE_INLINE void b128_store_rows16(const B128GemmParams &p, const uint32_t (&h)[8], int m0q, int rows, int col,
+                                        int lane, uint32_t *stage) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) stage[lane * kB128StagePitch + e] = h[e];
+    __syncwarp();
+    const int c = lane & 15;
+    for (int r = lane >> 4; r < rows; r += 2)
+        if (col + c < p.N)
+            p.C[(int64_t)(m0q + r) * p.ldc + col + c] =
+                (uint16_t)(stage[r * kB128StagePitch + (c >> 1)] >> (16 * (c & 1)));
+    __syncwarp();
+}
+
+MX_DEVICE_INLINE uint32_t bf16_pair(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // CH: 32-column chunks per drain warp (4: tiles of up to 256 columns and two
-// partial buffers; 2: up to 128 columns and four partial buffers).
-template <bool PAIR, int CH, bool GROUPED>
+// partial buffers; 2: up to 128 columns and four partial buffers).  ONE: a
+// warp's columns lie in one 128-column scale block (bn a power of two).
+// VIA_TMEM: results are stored through TMEM (GELU, rows of C off 16 bytes); a
+// variant of its own, since that path in the same code costs the loop before it
+// registers (8192^3: 1200 against 1090 cycles per block).
+template <bool PAIR, int CH, bool GROUPED, bool ONE, bool VIA_TMEM>
 __global__ void __launch_bounds__(kB128Threads, 1)
     gemm_b128_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmC, const B128GemmParams p) {
+                     const B128GemmParams p) {
     constexpr int kPartialCols = CH * 64;
     constexpr int NP = 512 / kPartialCols;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int S = p.stages;
     uint8_t *smem_a = smem, *smem_b = smem + S * p.a_bytes;
-    uint8_t *staging = smem_b + S * p.b_bytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(staging + kB128StagingBytes);   // the pair leader's count both CTAs
+    float *scale_ring = reinterpret_cast<float *>(smem_b + S * p.b_bytes);   // [slots][kB128SlotFloats]
+    uint8_t *staging = reinterpret_cast<uint8_t *>(scale_ring + kB128ScaleSlots * kB128SlotFloats);
+    uint64_t *full = reinterpret_cast<uint64_t *>(staging + p.staging_bytes);   // the pair leader's count both CTAs
     uint64_t *empty = full + kB128MaxStages;
     uint64_t *pfull = empty + kB128MaxStages;   // [NP]
     uint64_t *pempty = pfull + 4;               // [NP], the leader's count both CTAs' drain warps
-    uint64_t *mma_done = pempty + 4;
+    uint64_t *sfull = pempty + 4;               // [kB128ScaleGroups]
+    uint64_t *sempty = sfull + kB128ScaleGroups;
+    uint64_t *mma_done = sempty + kB128ScaleGroups;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -189,12 +214,15 @@ __global__ void __launch_bounds__(kB128Threads, 1)
             mbar_init(&pfull[i], 1);
             mbar_init(&pempty[i], (PAIR ? 2 : 1) * kB128DrainWarps);
         }
+        for (int i = 0; i < kB128ScaleGroups; ++i) {
+            mbar_init(&sfull[i], 64);
+            mbar_init(&sempty[i], kB128DrainWarps);
+        }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        if (p.use_tma_store) tma_prefetch_desc(&tmC);
     }
     if (warp == 1) {
         if (PAIR) {
@@ -210,6 +238,8 @@ __global__ void __launch_bounds__(kB128Threads, 1)
     if (PAIR) cluster_sync();   // both CTAs' barriers exist before anyone signals them
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), pfull0 = smem_u32(pfull),
+                   pempty0 = smem_u32(pempty), sfull0 = smem_u32(sfull), sempty0 = smem_u32(sempty);
     griddep_wait();
 
     if (warp < 4) {
@@ -226,7 +256,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                 const int a_row = t.row0 + (PAIR ? 128 * (int)rank : 0);
                 const int b_row = t.group * p.N + t.n0 + (PAIR ? (p.bn / 2) * (int)rank : 0);
                 for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!mbar_wait_bounded(&empty[s], ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
+                    if (!mbar_wait_at(empty0 + 8u * (uint32_t)s, ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
                         stop = true;
                         break;
                     }
@@ -253,7 +283,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
             // copies in flight land before this CTA (the leader, for both) may leave
             if (rank == 0)
                 for (int u = max(0, used - S); u < used; ++u)
-                    mbar_wait_bounded(&full[u % S], (uint32_t)((u / S) & 1), p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
+                    mbar_wait_at(full0 + 8u * (uint32_t)(u % S), (uint32_t)((u / S) & 1), p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
         } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------- MMA issuer
             const uint64_t desc = smem_desc(0, 16, 1024, 2);
@@ -264,12 +294,13 @@ __global__ void __launch_bounds__(kB128Threads, 1)
             B128Tiles<GROUPED> tiles(p, lane);
             int s = 0, pi = 0;
             uint32_t ph = 0, pph = 0;
-            bool stop = false;
+            bool stop = false, full_ok = false, empty_ok = false;   // the next block's barriers, as asked ahead
             B128Tile t;
             for (int i = worker; !stop && tiles.at(i, t); i += workers) {
                 for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!mbar_wait_bounded(&pempty[pi], pph ^ 1u, p.wait_limit_ns, SITE_GEMM_MMA_ACC_EMPTY, abort_flag) ||
-                        !mbar_wait_bounded(&full[s], ph, p.wait_limit_ns, SITE_GEMM_MMA_FULL, abort_flag)) {
+                    if ((!full_ok && !mbar_wait_at(full0 + 8u * (uint32_t)s, ph, p.wait_limit_ns, SITE_GEMM_MMA_FULL, abort_flag)) ||
+                        (!empty_ok &&
+                         !mbar_wait_at(pempty0 + 8u * (uint32_t)pi, pph ^ 1u, p.wait_limit_ns, SITE_GEMM_MMA_ACC_EMPTY, abort_flag))) {
                         stop = true;
                         break;
                     }
@@ -282,11 +313,11 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                         else tc_mma_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, leader);
                     }
                     if (PAIR) {
-                        tc_commit_pair_if(&empty[s], 0x3, leader);
                         tc_commit_pair_if(&pfull[pi], 0x3, leader);
+                        tc_commit_pair_if(&empty[s], 0x3, leader);
                     } else {
-                        tc_commit_if(&empty[s], leader);
                         tc_commit_if(&pfull[pi], leader);
+                        tc_commit_if(&empty[s], leader);
                     }
                     if (++s == S) {
                         s = 0;
@@ -296,123 +327,218 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                         pi = 0;
                         pph ^= 1u;
                     }
+                    full_ok = mbar_test_at(full0 + 8u * (uint32_t)s, ph);
+                    empty_ok = mbar_test_at(pempty0 + 8u * (uint32_t)pi, pph ^ 1u);
                 }
             }
             if (PAIR) tc_commit_pair_if(mma_done, 0x3, leader);
             else tc_commit_if(mma_done, leader);
             __syncwarp();
+        } else if (warp >= 2) {
+            // -------------------------------------------------------- scales
+            const int r0 = threadIdx.x - 64;   // this thread's rows of the tile: r0 and r0 + 64
+            B128Tiles<GROUPED> tiles(p, lane);
+            const int last_sb = (p.N + 127) / 128 - 1;
+            int g = 0;
+            uint32_t ph = 0;
+            bool stop = false;
+            B128Tile t;
+            for (int i = worker; !stop && tiles.at(i, t); i += workers) {
+                const int row0 = t.row0 + (PAIR ? 128 * (int)rank : 0);
+                const int row_end = min(t.row_end, t.row0 + (1 << p.bm_shift));
+                const bool on0 = row0 + r0 < row_end, on1 = row0 + r0 + 64 < row_end;
+                const float *sa = p.sa + row0 + r0;
+                // threads 0 .. 2: the column blocks' scales
+                const bool on_b = r0 < 3;
+                const float *sb = p.sb + (int64_t)t.group * p.sb_step + (int64_t)min((t.n0 >> 7) + r0, last_sb) * p.num_kb;
+                for (int kb = 0; kb < p.num_kb; kb += kB128ScaleGroup) {
+                    if (!mbar_wait_at(sempty0 + 8u * (uint32_t)g, ph ^ 1u, p.wait_limit_ns, SITE_GEMM_SF_EMPTY, abort_flag)) {
+                        stop = true;
+                        break;
+                    }
+                    float *f = scale_ring + g * kB128ScaleGroup * kB128SlotFloats;
+#pragma unroll
+                    for (int j = 0; j < kB128ScaleGroup; ++j, f += kB128SlotFloats)
+                        if (kb + j < p.num_kb) {
+                            if (on0) cp_async4(f + r0, sa);
+                            if (on1) cp_async4(f + r0 + 64, sa + 64);
+                            if (on_b) cp_async4(f + 128 + r0, sb);
+                            sa += p.sa_pitch;
+                            ++sb;
+                        }
+                    cp_async_arrive(&sfull[g]);
+                    if (++g == kB128ScaleGroups) {
+                        g = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            cp_async_wait_all();
         }
     } else {
         // ------------------------------------------------------------ drain
         if (CH == 4) setmaxnreg_inc<kB128DrainRegs>();
         const int q = warp & 3;                       // TMEM lane quadrant
         const int half = (warp - 4) >> 2;
-        const int n_chunks = p.bn / 32;
-        const int c0 = half == 0 ? 0 : (n_chunks + 1) / 2;                          // this warp's chunks
-        const int nc = half == 0 ? (n_chunks + 1) / 2 : n_chunks - (n_chunks + 1) / 2;
+        // this warp's chunks: CH of them whatever bn is (the loop below has to be
+        // straight code); those past bn hold nothing that is stored
+        const int c0 = half * CH;
+        const int nc = min(CH, p.bn / 32 - c0);
         const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(32 * c0);
-        uint8_t *bufs = staging + (warp - 4) * 2 * kEpiChunkBytes;
-        const uint32_t pempty0 = PAIR ? mapa_shared(smem_u32(&pempty[0]), 0) : 0u;
-        const int last_sb = (p.N + 127) / 128 - 1;
+        uint32_t *stage = reinterpret_cast<uint32_t *>(staging) + (warp - 4) * 32 * kB128StagePitch;
+        const uint32_t pempty_leader = PAIR ? mapa_shared(pempty0, 0) : 0u;
+        const uint32_t ring = smem_u32(scale_ring);
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        auto release = [&](uint32_t buf) {
+            tc_fence_before();
+            __syncwarp();
+            if (PAIR) mbar_arrive_cluster_if(pempty_leader + 8u * buf, lead);
+            else mbar_arrive_at_if(pempty0 + 8u * buf, lead);
+        };
         B128Tiles<GROUPED> tiles(p, lane);
-        int pi = 0;
-        uint32_t pph = 0, nstore = 0;
-        bool stop = false;
+        uint32_t pi = 0, pph = 0, g = 0, sph = 0;
+        bool stop = false, ready = false;   // ready: the next partial buffer is full, as asked ahead
         B128Tile t;
         for (int i = worker; !stop && tiles.at(i, t); i += workers) {
             const int m0q = t.row0 + (PAIR ? 128 * (int)rank : 0) + 32 * q;
             const int row_end = min(t.row_end, t.row0 + (1 << p.bm_shift));
             const bool any = m0q < row_end;           // warp-uniform
-            const int row = m0q + lane;
-            // the (at most two) 128-column scale blocks under this warp's columns
-            const int nb0 = (t.n0 + 32 * c0) >> 7;
-            const int split = (4 * (nb0 + 1)) - ((t.n0 >> 5) + c0);   // chunks in the first of them
-            const float *sa = p.sa + row;
-            const float *sb0 = p.sb + (int64_t)t.group * p.sb_step + (int64_t)min(nb0, last_sb) * p.num_kb;
-            const float *sb1 = p.sb + (int64_t)t.group * p.sb_step + (int64_t)min(nb0 + 1, last_sb) * p.num_kb;
-            const bool row_ok = row < row_end;
+            // the (at most two) 128-column scale blocks under this warp's
+            // columns: the first one's place in the ring slot, and how many of
+            // the warp's chunks lie in it
+            const int b0 = ((t.n0 + 32 * c0) >> 7) - (t.n0 >> 7);
+            const int split = ONE ? CH : 4 * (b0 + 1 + (t.n0 >> 7)) - ((t.n0 >> 5) + c0);
             uint64_t acc[CH * 16];
 #pragma unroll
             for (int c = 0; c < CH * 16; ++c) acc[c] = 0u;
-            // scales are fetched four blocks ahead of their use
-            float f0[4], f1[4];
-            auto fetch = [&](int kb, float &a, float &b) {
-                a = b = 0.0f;
-                if (row_ok && kb < p.num_kb) {
-                    const float s = __ldg(sa + (int64_t)kb * p.sa_pitch);
-                    a = s * __ldg(sb0 + kb);
-                    b = s * __ldg(sb1 + kb);
+            // VIA_TMEM: a tile keeps its last partial buffer until its results are stored
+            uint32_t last = 0;
+#pragma unroll 1
+            for (int kb0 = 0; kb0 < p.num_kb; kb0 += kB128ScaleGroup) {
+                if (!mbar_wait_at(sfull0 + 8u * g, sph, p.wait_limit_ns, SITE_GEMM_SF_FULL, abort_flag)) {
+                    stop = true;
+                    break;
                 }
-            };
-#pragma unroll
-            for (int j = 0; j < 4; ++j) fetch(j, f0[j], f1[j]);
-            for (int kb0 = 0; kb0 < p.num_kb && !stop; kb0 += 4) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (kb0 + j < p.num_kb) {
-                        if (!mbar_wait_bounded(&pfull[pi], pph, p.wait_limit_ns, SITE_GEMM_EPI_ACC, abort_flag)) {
-                            stop = true;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t F0 = pk2(f0[j], f0[j]), F1 = pk2(f1[j], f1[j]);
-                        const uint32_t t_p = t_lane + (uint32_t)(pi * kPartialCols);
-                        auto release = [&] {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (PAIR) mbar_arrive_cluster(pempty0 + 8u * (uint32_t)pi);
-                                else mbar_arrive(&pempty[pi]);
-                            }
-                        };
-#pragma unroll
-                        for (int h = 0; h < CH / 2; ++h) {
-                            uint32_t r[2][32];
-                            const bool on0 = any && 2 * h < nc, on1 = any && 2 * h + 1 < nc;   // warp-uniform
-                            if (on0) tmem_ld32(t_p + 64 * h, r[0]);
-                            if (on1) tmem_ld32(t_p + 64 * h + 32, r[1]);
-                            if (on0) tmem_wait_ld();
-                            if (h == CH / 2 - 1) release();
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                if (e == 0 ? on0 : on1) {
-                                    const uint64_t F = 2 * h + e < split ? F0 : F1;
-#pragma unroll
-                                    for (int c = 0; c < 16; ++c)
-                                        acc[32 * h + 16 * e + c] =
-                                            fma2(pk2(__uint_as_float(r[e][2 * c]), __uint_as_float(r[e][2 * c + 1])), F,
-                                                 acc[32 * h + 16 * e + c]);
-                                }
-                            }
-                        }
-                        if (++pi == NP) {
-                            pi = 0;
-                            pph ^= 1u;
-                        }
-                        fetch(kb0 + j + 4, f0[j], f1[j]);
+                uint32_t f = ring + g * (uint32_t)(kB128ScaleGroup * kB128SlotFloats * 4);
+                const int kb1 = min(kb0 + kB128ScaleGroup, p.num_kb);
+#pragma unroll 1
+                for (int kb = kb0; kb < kb1; ++kb, f += kB128SlotFloats * 4) {
+                    const float fa = ld_shared_f32(f + 4u * (uint32_t)(32 * q + lane));
+                    const float fb0 = ld_shared_f32(f + 4u * (uint32_t)(128 + b0));
+                    const float fb1 = ONE ? 0.0f : ld_shared_f32(f + 4u * (uint32_t)(129 + b0));   // (a fourth is never used)
+                    if (!ready && !mbar_wait_at(pfull0 + 8u * pi, pph, p.wait_limit_ns, SITE_GEMM_EPI_ACC, abort_flag)) {
+                        stop = true;
+                        break;
                     }
+                    tc_fence_after();
+                    const uint32_t cur = pi, t_p = t_lane + pi * (uint32_t)kPartialCols;
+                    if (++pi == NP) {
+                        pi = 0;
+                        pph ^= 1u;
+                    }
+                    if (any) {
+                        const float f0 = fa * fb0, f1 = ONE ? f0 : fa * fb1;
+                        const uint64_t F0 = pk2(f0, f0), F1 = pk2(f1, f1);
+                        // Straight code: the loads of one chunk run while the
+                        // previous one is folded in.  (With a test per chunk the
+                        // block took 565 cycles instead of 350, of the 512 that
+                        // its MMAs take.)
+#pragma unroll
+                        for (int h = 0; h < CH; ++h) {
+                            uint32_t r[32];
+                            tmem_ld32(t_p + 32 * h, r);
+                            tmem_wait_ld();
+                            if (h == CH - 1) {
+                                if (!VIA_TMEM || kb + 1 < p.num_kb) release(cur);
+                                ready = mbar_test_at(pfull0 + 8u * pi, pph);
+                            }
+                            const uint64_t F = ONE || h < split ? F0 : F1;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                acc[16 * h + c] = fma2(pk2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), F,
+                                                       acc[16 * h + c]);
+                        }
+                    } else {
+                        release(cur);
+                        ready = false;
+                    }
+                    if (VIA_TMEM) last = cur;
+                }
+                if (stop) break;
+                mbar_arrive_at_if(sempty0 + 8u * g, lead);
+                if (++g == kB128ScaleGroups) {
+                    g = 0;
+                    sph ^= 1u;
                 }
             }
             if (stop || !any) continue;
             // -------------------------------------------------------- epilogue
+            const int row = m0q + lane;
+            const bool row_ok = row < row_end;
+            const int col0 = t.n0 + 32 * c0;
+            if (!VIA_TMEM) {
+                if (row_ok) {
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                const int col = t.n0 + 32 * (c0 + ch);
-                if (ch < nc && col < p.N) {
-                    uint32_t packed[16];
+                    for (int c = 0; c < CH * 2; ++c) {
+                        if (c < 2 * nc && col0 + 16 * c < p.N) {
+                            uint32_t h[8];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float x0, x1;
-                        upk2(acc[16 * ch + c], x0, x1);
-                        if (p.epilogue == 1) gelu_erf2(x0, x1);
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-                        packed[c] = *reinterpret_cast<const uint32_t *>(&h);
+                            for (int e = 0; e < 8; ++e) {
+                                float x0, x1;
+                                upk2(acc[8 * c + e], x0, x1);
+                                h[e] = bf16_pair(x0, x1);
+                            }
+                            b128_store_row16(p, h, row, col0 + 16 * c);
+                        }
                     }
-                    b128_store_chunk(p, &tmC, packed, m0q, row_end, col, lane, bufs, nstore);
                 }
+                __syncwarp();
+            } else {
+                // The sums go back to TMEM, so that one short loop can index
+                // them: unrolled over 128 registers, GELU's code outgrows the
+                // instruction cache.
+                const uint32_t t_p = t_lane + last * (uint32_t)kPartialCols;
+#pragma unroll
+                for (int c = 0; c < CH * 2; ++c) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        r[2 * e] = (uint32_t)acc[8 * c + e];
+                        r[2 * e + 1] = (uint32_t)(acc[8 * c + e] >> 32);
+                    }
+                    tmem_st16(t_p + 16 * c, r);
+                }
+                tmem_wait_st();
+#pragma unroll 1
+                for (int c = 0; c < nc && col0 + 32 * c < p.N; ++c) {
+                    uint32_t r[32], h[2][8];
+                    tmem_ld32(t_p + 32 * c, r);
+                    tmem_wait_ld();
+                    if (p.epilogue == 1) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float x0 = __uint_as_float(r[2 * e]), x1 = __uint_as_float(r[2 * e + 1]);
+                            gelu_erf2(x0, x1);
+                            h[e >> 3][e & 7] = bf16_pair(x0, x1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            h[e >> 3][e & 7] = bf16_pair(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int col = col0 + 32 * c + 16 * e;
+                        if (p.vec_store == 0)
+                            b128_store_rows16(p, h[e], m0q, min(32, row_end - m0q), col, lane, stage);
+                        else if (row_ok && col < p.N)
+                            b128_store_row16(p, h[e], row, col);
+                    }
+                    __syncwarp();
+                }
+                release(last);
             }
         }
-        if (lane == 0) bulk_wait_group_all();
     }
 
     tc_fence_before();
@@ -420,7 +546,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
     if (warp == 1) {
         tc_fence_after();
         // every MMA (of the pair) has completed once mma_done has fired
-        mbar_wait_bounded(mma_done, 0, p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
+        mbar_wait_at(smem_u32(mma_done), 0, p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
         if (PAIR) tmem_dealloc_pair(tmem, 512);
         else tmem_dealloc(tmem, 512);
     }

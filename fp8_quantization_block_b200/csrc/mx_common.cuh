@@ -118,6 +118,65 @@ MX_DEVICE_INLINE bool mbar_wait_bounded(uint64_t *bar, uint32_t parity, uint64_t
     }
 }
 
+// Barriers by their shared-memory address (32 bits), for loops where forming it
+// from a pointer each time would show.
+//
+// Wait with the thread suspended by the hardware (up to 20 us at a time)
+// instead of polling: the retries' instructions would take issue slots from the
+// warps that compute, and reading the clock before the first retry costs more
+// than most waits last.  The limit counts from the first retry.
+MX_DEVICE_INLINE bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+MX_DEVICE_INLINE bool mbar_wait_at(uint32_t bar, uint32_t parity, uint64_t limit_ns, unsigned site, volatile int *abort) {
+    if (mbar_try_wait_at(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (;;) {
+        if (mbar_try_wait_at(bar, parity)) return true;
+        if (abort != nullptr && *abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > limit_ns) {
+            record_error(DEVERR_TIMEOUT, site);
+            if (abort != nullptr) *abort = 1;
+            return false;
+        }
+    }
+}
+// Has the phase completed?  No waiting: asked ahead of time, so that the answer's
+// latency runs beside other work.
+MX_DEVICE_INLINE bool mbar_test_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Arrive by the threads whose `on` flag is set, without a branch.
+MX_DEVICE_INLINE void mbar_arrive_at_if(uint32_t bar, uint32_t on) {
+    asm volatile("{\n\t.reg .b64 st;\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar),
+                 "r"(on)
+                 : "memory");
+}
+MX_DEVICE_INLINE float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // Programmatic dependent launch.  A kernel launched with programmatic stream
 // serialization may start while the previous kernel in the stream is still
 // running; griddep_wait() returns once that kernel has completed and its
@@ -261,6 +320,17 @@ MX_DEVICE_INLINE void bulk_load(void *smem_dst, const void *src, uint32_t bytes,
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
+
+// Copy 4 bytes of global memory into shared memory asynchronously (no
+// alignment beyond the 4 bytes), and arrive on an mbarrier once all such copies
+// that this thread has issued are done (one of the barrier's own count).
+MX_DEVICE_INLINE void cp_async4(void *smem_dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
+}
+MX_DEVICE_INLINE void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+MX_DEVICE_INLINE void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // 3D tiled TMA load (no multicast) into this CTA's shared memory.
 MX_DEVICE_INLINE void tma_load_3d(void *smem_dst, const void *tmap, int32_t x, int32_t y, int32_t z, uint64_t *bar) {
@@ -425,6 +495,12 @@ MX_DEVICE_INLINE uint32_t mapa_shared(uint32_t local_saddr, uint32_t rank) {
 // about a thousand cycles per arrive here and is not needed for that order.
 MX_DEVICE_INLINE void mbar_arrive_cluster(uint32_t cluster_saddr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr) : "memory");
+}
+MX_DEVICE_INLINE void mbar_arrive_cluster_if(uint32_t cluster_saddr, uint32_t on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_saddr),
+                 "r"(on)
+                 : "memory");
 }
 // 2D tiled TMA load into this CTA's shared memory whose completion is signalled
 // on an mbarrier of the pair's leader CTA (cta_group::2 form, no multicast).

@@ -56,10 +56,10 @@ B128Config b128_config(int64_t n, int sms, bool allow_pair, int max_shift, MBloc
     return best;
 }
 
-template <bool PAIR, int CH, bool GROUPED>
-mx_status launch_b128_t(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tc, const B128GemmParams &p,
-                        int workers, size_t smem, cudaStream_t st) {
-    const auto kern = gemm_b128_kernel<PAIR, CH, GROUPED>;
+template <bool PAIR, int CH, bool GROUPED, bool ONE, bool VIA>
+mx_status launch_b128_t(const CUtensorMap &ta, const CUtensorMap &tb, const B128GemmParams &p, int workers, size_t smem,
+                        cudaStream_t st) {
+    const auto kern = gemm_b128_kernel<PAIR, CH, GROUPED, ONE, VIA>;
     if (smem_limit_once(reinterpret_cast<const void *>(kern), kSmemLimit) != cudaSuccess) return MX_ERR_CUDA;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(PAIR ? 2 * workers : workers), 1, 1), kB128Threads, smem, st, attr);
@@ -70,7 +70,7 @@ mx_status launch_b128_t(const CUtensorMap &ta, const CUtensorMap &tb, const CUte
         c.val.clusterDim.y = 1;
         c.val.clusterDim.z = 1;
     }
-    cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, p);
+    cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
     return last_launch();
 }
 
@@ -99,16 +99,16 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     const int b_rows = cfg.pair ? cfg.bn / 2 : cfg.bn;
     p.a_bytes = a_rows * kStageKBytes;
     p.b_bytes = b_rows * kStageKBytes;
-    const int fixed = 1024 + kB128StagingBytes + (2 * kB128MaxStages + 9) * 8 + 16;
+    const auto base = reinterpret_cast<uintptr_t>(C);
+    p.vec_store = ldc % 16 == 0 && base % 32 == 0 ? 2 : (ldc % 8 == 0 && base % 16 == 0 ? 1 : 0);
+    p.staging_bytes = p.vec_store ? 0 : kB128StagingBytes;
+    const int fixed = kB128FixedBytes + p.staging_bytes;
     p.stages = (kSmemLimit - fixed) / (p.a_bytes + p.b_bytes);
     if (p.stages > kB128MaxStages) p.stages = kB128MaxStages;
     const size_t smem = (size_t)fixed + (size_t)p.stages * (p.a_bytes + p.b_bytes);
-    CUtensorMap ta, tb, tc;
+    CUtensorMap ta, tb;
     if (!make_tmap_u8(&ta, A->codes, M, K, a_rows)) return MX_ERR_CUDA;
     if (!make_tmap_u8(&tb, B->codes, G * N, K, b_rows)) return MX_ERR_CUDA;
-    const bool tma_store = (ldc % 8 == 0) && aligned16(C);
-    memset(&tc, 0, sizeof(tc));
-    if (tma_store && !make_tmap_c(&tc, C, M, N, ldc)) return MX_ERR_CUDA;
     p.sa = reinterpret_cast<const float *>(A->scales);
     p.sb = reinterpret_cast<const float *>(B->scales);
     p.C = C;
@@ -123,7 +123,6 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     p.m_blocks = (int)cdiv(M, (int64_t)1 << cfg.bm_shift);
     p.n_blocks = (int)cdiv(N, cfg.bn);
     p.epilogue = epilogue;
-    p.use_tma_store = tma_store ? 1 : 0;
     p.skip_producer = g_skip_producer.load();
     p.wait_limit_ns = g_wait_limit_ns.load();
     if (groups) p.groups = Groups{groups->offsets, groups->count, (int)M};
@@ -134,16 +133,23 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     int64_t workers = cfg.pair ? sms / 2 : sms;
     if (cap > 0 && cap < sms) workers = cfg.pair ? (cap + 1) / 2 : cap;
     if (workers > tiles) workers = tiles;
-    const bool wide = cfg.bn > 128;
-#define MX_LAUNCH(PAIR, CH)                                                                             \
-    return groups ? launch_b128_t<PAIR, CH, true>(ta, tb, tc, p, (int)workers, smem, st)               \
-                  : launch_b128_t<PAIR, CH, false>(ta, tb, tc, p, (int)workers, smem, st)
+    const bool one = (cfg.bn & (cfg.bn - 1)) == 0;
+    const bool via = epilogue == MX_EPI_GELU || p.vec_store == 0;
+#define MX_LAUNCH(PAIR, CH, ONE)                                                                       \
+    return groups ? (via ? launch_b128_t<PAIR, CH, true, ONE, true>(ta, tb, p, (int)workers, smem, st)      \
+                         : launch_b128_t<PAIR, CH, true, ONE, false>(ta, tb, p, (int)workers, smem, st))    \
+                  : (via ? launch_b128_t<PAIR, CH, false, ONE, true>(ta, tb, p, (int)workers, smem, st)     \
+                         : launch_b128_t<PAIR, CH, false, ONE, false>(ta, tb, p, (int)workers, smem, st))
     if (cfg.pair) {
-        if (wide) MX_LAUNCH(true, 4);
-        MX_LAUNCH(true, 2);
+        if (cfg.bn == 256) MX_LAUNCH(true, 4, true);
+        if (cfg.bn > 128) MX_LAUNCH(true, 4, false);
+        if (one) MX_LAUNCH(true, 2, true);
+        MX_LAUNCH(true, 2, false);
     }
-    if (wide) MX_LAUNCH(false, 4);
-    MX_LAUNCH(false, 2);
+    if (cfg.bn == 256) MX_LAUNCH(false, 4, true);
+    if (cfg.bn > 128) MX_LAUNCH(false, 4, false);
+    if (one) MX_LAUNCH(false, 2, true);
+    MX_LAUNCH(false, 2, false);
 #undef MX_LAUNCH
 }
 
