@@ -45,10 +45,9 @@ constexpr int kB128Threads = 384;
 constexpr int kB128DrainWarps = 8;
 constexpr int kB128MaxStages = 16;
 // Registers per thread; the sum over the three warpgroups is what the block is
-// launched with (384 threads at 168).  Measured on 8192^3: 200 for the drain
-// warps 644 us, 216 740 us (the scheduler then overlaps more loads and spills
-// instead), 176 688 us.
-constexpr int kB128DrainRegs = 200, kB128OtherRegs = 104;
+// launched with (384 threads at 168).  8192^3 in a seconds-long loop: 208 for
+// the drain warps 656 us, 192 667 us; 216 leaves the other warps' code spills.
+constexpr int kB128DrainRegs = 208, kB128OtherRegs = 88;
 static_assert(2 * kB128DrainRegs + kB128OtherRegs <= 3 * 168, "register split");
 
 struct B128GemmParams {
@@ -173,12 +172,11 @@ MX_DEVICE_INLINE uint32_t bf16_pair(float a, float b) {
 }
 
 // CH: 32-column chunks per drain warp (4: tiles of up to 256 columns and two
-// partial buffers; 2: up to 128 columns and four partial buffers).  ONE: a
-// warp's columns lie in one 128-column scale block (bn a power of two).
+// partial buffers; 2: up to 128 columns and four partial buffers).
 // VIA_TMEM: results are stored through TMEM (GELU, rows of C off 16 bytes); a
 // variant of its own, since that path in the same code costs the loop before it
 // registers (8192^3: 1200 against 1090 cycles per block).
-template <bool PAIR, int CH, bool GROUPED, bool ONE, bool VIA_TMEM>
+template <bool PAIR, int CH, bool GROUPED, bool VIA_TMEM>
 __global__ void __launch_bounds__(kB128Threads, 1)
     gemm_b128_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const B128GemmParams p) {
@@ -389,11 +387,11 @@ __global__ void __launch_bounds__(kB128Threads, 1)
         const uint32_t pempty_leader = PAIR ? mapa_shared(pempty0, 0) : 0u;
         const uint32_t ring = smem_u32(scale_ring);
         const uint32_t lead = lane == 0 ? 1u : 0u;
-        auto release = [&](uint32_t buf) {
+        auto release = [&](uint32_t buf, uint32_t on) {   // without a branch
             tc_fence_before();
             __syncwarp();
-            if (PAIR) mbar_arrive_cluster_if(pempty_leader + 8u * buf, lead);
-            else mbar_arrive_at_if(pempty0 + 8u * buf, lead);
+            if (PAIR) mbar_arrive_cluster_if(pempty_leader + 8u * buf, lead & on);
+            else mbar_arrive_at_if(pempty0 + 8u * buf, lead & on);
         };
         B128Tiles<GROUPED> tiles(p, lane);
         uint32_t pi = 0, pph = 0, g = 0, sph = 0;
@@ -407,7 +405,8 @@ __global__ void __launch_bounds__(kB128Threads, 1)
             // columns: the first one's place in the ring slot, and how many of
             // the warp's chunks lie in it
             const int b0 = ((t.n0 + 32 * c0) >> 7) - (t.n0 >> 7);
-            const int split = ONE ? CH : 4 * (b0 + 1 + (t.n0 >> 7)) - ((t.n0 >> 5) + c0);
+            const int split = 4 * (b0 + 1 + (t.n0 >> 7)) - ((t.n0 >> 5) + c0);
+            const uint32_t my_row = 4u * (uint32_t)(32 * q + lane), my_col = 4u * (uint32_t)(128 + b0);
             uint64_t acc[CH * 16];
 #pragma unroll
             for (int c = 0; c < CH * 16; ++c) acc[c] = 0u;
@@ -420,12 +419,11 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     break;
                 }
                 uint32_t f = ring + g * (uint32_t)(kB128ScaleGroup * kB128SlotFloats * 4);
+                float fa = ld_shared_f32(f + my_row), fb0 = ld_shared_f32(f + my_col);
+                float fb1 = ld_shared_f32(f + my_col + 4);   // (a fourth column block is never used)
                 const int kb1 = min(kb0 + kB128ScaleGroup, p.num_kb);
 #pragma unroll 1
-                for (int kb = kb0; kb < kb1; ++kb, f += kB128SlotFloats * 4) {
-                    const float fa = ld_shared_f32(f + 4u * (uint32_t)(32 * q + lane));
-                    const float fb0 = ld_shared_f32(f + 4u * (uint32_t)(128 + b0));
-                    const float fb1 = ONE ? 0.0f : ld_shared_f32(f + 4u * (uint32_t)(129 + b0));   // (a fourth is never used)
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!ready && !mbar_wait_at(pfull0 + 8u * pi, pph, p.wait_limit_ns, SITE_GEMM_EPI_ACC, abort_flag)) {
                         stop = true;
                         break;
@@ -437,29 +435,34 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                         pph ^= 1u;
                     }
                     if (any) {
-                        const float f0 = fa * fb0, f1 = ONE ? f0 : fa * fb1;
+                        // Straight code, nothing conditional: a chunk's load runs
+                        // while the one before it is folded in, and the next
+                        // block's scales and barrier are asked for on the way.
+                        // (The drain alone, on one SM: 565 cycles per block with a
+                        // test per chunk, 517 as a plain sequence, 476 like this,
+                        // of the 512 that the block's MMAs take.)
+                        uint32_t r[2][32];
+                        tmem_ld32(t_p, r[0]);
+                        const float f0 = fa * fb0, f1 = fa * fb1;
                         const uint64_t F0 = pk2(f0, f0), F1 = pk2(f1, f1);
-                        // Straight code: the loads of one chunk run while the
-                        // previous one is folded in.  (With a test per chunk the
-                        // block took 565 cycles instead of 350, of the 512 that
-                        // its MMAs take.)
+                        f += kb + 1 < kb1 ? (uint32_t)(kB128SlotFloats * 4) : 0u;
+                        fa = ld_shared_f32(f + my_row);
+                        fb0 = ld_shared_f32(f + my_col);
+                        fb1 = ld_shared_f32(f + my_col + 4);
 #pragma unroll
                         for (int h = 0; h < CH; ++h) {
-                            uint32_t r[32];
-                            tmem_ld32(t_p + 32 * h, r);
                             tmem_wait_ld();
-                            if (h == CH - 1) {
-                                if (!VIA_TMEM || kb + 1 < p.num_kb) release(cur);
-                                ready = mbar_test_at(pfull0 + 8u * pi, pph);
-                            }
-                            const uint64_t F = ONE || h < split ? F0 : F1;
+                            if (h + 1 < CH) tmem_ld32(t_p + 32 * (h + 1), r[(h + 1) & 1]);
+                            else release(cur, !VIA_TMEM || kb + 1 < p.num_kb ? 1u : 0u);
+                            if (h == (CH > 1 ? CH - 2 : 0)) ready = mbar_test_at(pfull0 + 8u * pi, pph);
+                            const uint64_t F = h < split ? F0 : F1;
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
-                                acc[16 * h + c] = fma2(pk2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), F,
-                                                       acc[16 * h + c]);
+                                acc[16 * h + c] = fma2(pk2(__uint_as_float(r[h & 1][2 * c]),
+                                                           __uint_as_float(r[h & 1][2 * c + 1])), F, acc[16 * h + c]);
                         }
                     } else {
-                        release(cur);
+                        release(cur, 1u);
                         ready = false;
                     }
                     if (VIA_TMEM) last = cur;
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     }
                     __syncwarp();
                 }
-                release(last);
+                release(last, 1u);
             }
         }
     }

@@ -56,10 +56,10 @@ B128Config b128_config(int64_t n, int sms, bool allow_pair, int max_shift, MBloc
     return best;
 }
 
-template <bool PAIR, int CH, bool GROUPED, bool ONE, bool VIA>
+template <bool PAIR, int CH, bool GROUPED, bool VIA>
 mx_status launch_b128_t(const CUtensorMap &ta, const CUtensorMap &tb, const B128GemmParams &p, int workers, size_t smem,
                         cudaStream_t st) {
-    const auto kern = gemm_b128_kernel<PAIR, CH, GROUPED, ONE, VIA>;
+    const auto kern = gemm_b128_kernel<PAIR, CH, GROUPED, VIA>;
     if (smem_limit_once(reinterpret_cast<const void *>(kern), kSmemLimit) != cudaSuccess) return MX_ERR_CUDA;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(PAIR ? 2 * workers : workers), 1, 1), kB128Threads, smem, st, attr);
@@ -133,23 +133,18 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     int64_t workers = cfg.pair ? sms / 2 : sms;
     if (cap > 0 && cap < sms) workers = cfg.pair ? (cap + 1) / 2 : cap;
     if (workers > tiles) workers = tiles;
-    const bool one = (cfg.bn & (cfg.bn - 1)) == 0;
-    const bool via = epilogue == MX_EPI_GELU || p.vec_store == 0;
-#define MX_LAUNCH(PAIR, CH, ONE)                                                                       \
-    return groups ? (via ? launch_b128_t<PAIR, CH, true, ONE, true>(ta, tb, p, (int)workers, smem, st)      \
-                         : launch_b128_t<PAIR, CH, true, ONE, false>(ta, tb, p, (int)workers, smem, st))    \
-                  : (via ? launch_b128_t<PAIR, CH, false, ONE, true>(ta, tb, p, (int)workers, smem, st)     \
-                         : launch_b128_t<PAIR, CH, false, ONE, false>(ta, tb, p, (int)workers, smem, st))
+    const bool via = epilogue == MX_EPI_GELU || p.vec_store == 0, wide = cfg.bn > 128;
+#define MX_LAUNCH(PAIR, CH)                                                                            \
+    return groups ? (via ? launch_b128_t<PAIR, CH, true, true>(ta, tb, p, (int)workers, smem, st)      \
+                         : launch_b128_t<PAIR, CH, true, false>(ta, tb, p, (int)workers, smem, st))    \
+                  : (via ? launch_b128_t<PAIR, CH, false, true>(ta, tb, p, (int)workers, smem, st)     \
+                         : launch_b128_t<PAIR, CH, false, false>(ta, tb, p, (int)workers, smem, st))
     if (cfg.pair) {
-        if (cfg.bn == 256) MX_LAUNCH(true, 4, true);
-        if (cfg.bn > 128) MX_LAUNCH(true, 4, false);
-        if (one) MX_LAUNCH(true, 2, true);
-        MX_LAUNCH(true, 2, false);
+        if (wide) MX_LAUNCH(true, 4);
+        MX_LAUNCH(true, 2);
     }
-    if (cfg.bn == 256) MX_LAUNCH(false, 4, true);
-    if (cfg.bn > 128) MX_LAUNCH(false, 4, false);
-    if (one) MX_LAUNCH(false, 2, true);
-    MX_LAUNCH(false, 2, false);
+    if (wide) MX_LAUNCH(false, 4);
+    MX_LAUNCH(false, 2);
 #undef MX_LAUNCH
 }
 
@@ -216,7 +211,7 @@ mx_status check_groups(const mx_groups *g) {
 template <int FMT>
 void launch_quantize_grouped(const GroupedQuantParams &p, int64_t bands, cudaStream_t st) {
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)cdiv(p.K, kQTileCols), (unsigned)bands, 1), kQThreads, 0, st, attr);
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(bands * p.slabs), 1, 1), kQThreads, 0, st, attr);
     cudaLaunchKernelEx(&cfg, quantize_grouped_kernel<FMT>, p);
 }
 
@@ -225,7 +220,7 @@ mx_status launch_route(const RouteParams &p, cudaStream_t st) {
     cudaLaunchAttribute attr[1];
     const size_t smem = (size_t)kRouteWarps * p.groups * sizeof(int);
     const int limit = kRouteWarps * kRouteMaxGroups * (int)sizeof(int);
-    if (p.n <= kRouteChunk) {
+    if (p.chunks <= 1) {
         if (smem_limit_once(reinterpret_cast<const void *>(route_small_kernel<ID>), limit) != cudaSuccess)
             return MX_ERR_CUDA;
         cudaLaunchConfig_t cfg = launch_cfg(dim3(1, 1, 1), kRouteThreads, smem, st, attr);
@@ -237,8 +232,6 @@ mx_status launch_route(const RouteParams &p, cudaStream_t st) {
         return MX_ERR_CUDA;
     cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)p.chunks, 1, 1), kRouteThreads, smem, st, attr);
     cudaLaunchKernelEx(&cfg, route_count_kernel<ID>, p);
-    cudaLaunchConfig_t one = launch_cfg(dim3(1, 1, 1), kRouteThreads, 0, st, attr);
-    cudaLaunchKernelEx(&one, route_scan_kernel, p);
     cudaLaunchKernelEx(&cfg, route_place_kernel<ID>, p);
     return last_launch();
 }
@@ -251,7 +244,6 @@ mx_status quantize_b128(int fmt, const uint16_t *src, int64_t M, int64_t K, int6
     B128QuantParams p{};
     p.src = src;
     p.ld = ld;
-    p.src_rows = M;
     p.M = M;
     p.K = K;
     p.codes = static_cast<uint8_t *>(dst->codes);
@@ -259,8 +251,8 @@ mx_status quantize_b128(int fmt, const uint16_t *src, int64_t M, int64_t K, int6
     p.pitch = fmt == MX_FP8_B128 ? b128_pitch(M) : K / 128;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(K / 128), (unsigned)cdiv(M, kQTileRows), 1), kQThreads, 0, st, attr);
-    if (fmt == MX_FP8_B128) cudaLaunchKernelEx(&cfg, quantize_b128_kernel<false, false>, p);
-    else cudaLaunchKernelEx(&cfg, quantize_b128_kernel<true, false>, p);
+    if (fmt == MX_FP8_B128) cudaLaunchKernelEx(&cfg, quantize_b128_kernel<false>, p);
+    else cudaLaunchKernelEx(&cfg, quantize_b128_kernel<true>, p);
     return last_launch();
 }
 
@@ -318,27 +310,9 @@ mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, i
     if (ld_src < K || (ld_src & 7) != 0) return MX_ERR_MISALIGNED;
     if (!aligned16(src_bf16) || !aligned16(dst->codes) || !aligned16(dst->scales)) return MX_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(row_index) & 3u) != 0) return MX_ERR_MISALIGNED;
-    const int64_t bands = fmt == MX_FP8_B128 ? cdiv(T, kQTileRows) : group_bands(T, groups->count);
-    if (T > INT32_MAX || bands > 65535) return MX_ERR_UNSUPPORTED_SHAPE;
+    const int64_t bands = group_bands(T, groups->count), tiles = cdiv(K, kQTileCols);
+    if (T > INT32_MAX || src_rows > INT32_MAX || bands * tiles > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (fmt == MX_FP8_B128) {
-        B128QuantParams p{};
-        p.src = static_cast<const uint16_t *>(src_bf16);
-        p.ld = ld_src;
-        p.src_rows = src_rows;
-        p.row_index = row_index;
-        p.offsets = groups->offsets;
-        p.groups = groups->count;
-        p.M = T;
-        p.K = K;
-        p.codes = static_cast<uint8_t *>(dst->codes);
-        p.scales = reinterpret_cast<float *>(dst->scales);
-        p.pitch = b128_pitch(T);
-        cudaLaunchAttribute attr[1];
-        cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(K / 128), (unsigned)bands, 1), kQThreads, 0, st, attr);
-        cudaLaunchKernelEx(&cfg, quantize_b128_kernel<false, true>, p);
-        return last_launch();
-    }
     GroupedQuantParams p{};
     p.src = static_cast<const uint16_t *>(src_bf16);
     p.ld = ld_src;
@@ -351,7 +325,16 @@ mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, i
     p.sf_tiles_k = cdiv(K / fmt_block(fmt), 4);
     p.gscale = gscale_in;
     p.gscale_out = gscale_in == dst->gscale ? nullptr : dst->gscale;
+    p.pitch = b128_pitch(T);
+    // K tiles per CTA: up to four, as long as every SM has a few CTAs
+    p.slab = (int)(bands * tiles / (4 * num_sms()));
+    if (p.slab > 4) p.slab = 4;
+    if (p.slab < 1) p.slab = 1;
+    p.slabs = (int)cdiv(tiles, p.slab);
+    // a gathered source that does not stay in L2 beside the output
+    p.interleave = row_index != nullptr && src_rows * K * 2 > (int64_t)32 << 20 ? 1 : 0;
     switch (fmt) {
+    case MX_FP8_B128: launch_quantize_grouped<FMT_B128>(p, bands, st); break;
     case MX_MXFP8_E4M3: launch_quantize_grouped<FMT_E4M3>(p, bands, st); break;
     case MX_MXFP8_E5M2: launch_quantize_grouped<FMT_E5M2>(p, bands, st); break;
     case MX_MXFP4: launch_quantize_grouped<FMT_MXFP4>(p, bands, st); break;
@@ -393,8 +376,8 @@ mx_status mx_gemm_grouped(const mx_tensor *A, const mx_tensor *B, const mx_group
 
 size_t mx_route_workspace_bytes(int64_t tokens, int choices, int groups) {
     if (tokens < 0 || choices < 1 || groups < 1 || tokens > INT32_MAX / choices) return 0;
-    const int64_t n = tokens * choices;
-    return n <= kRouteChunk ? 0 : (size_t)(cdiv(n, kRouteChunk) * groups) * sizeof(int32_t);
+    const int64_t n = tokens * choices, chunks = cdiv(n, route_chunk(n));
+    return chunks <= 1 ? 0 : (size_t)(chunks * groups) * sizeof(int32_t);
 }
 
 mx_status mx_route(const void *ids, int id_bits, int64_t tokens, int choices, int groups, int32_t *offsets,
@@ -418,7 +401,8 @@ mx_status mx_route(const void *ids, int id_bits, int64_t tokens, int choices, in
     p.row_token = row_token;
     p.slot = slot;
     p.counts = static_cast<int32_t *>(workspace);
-    p.chunks = (int)cdiv(p.n, kRouteChunk);
+    p.chunk = route_chunk(p.n);
+    p.chunks = (int)cdiv(p.n, p.chunk);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return id_bits == 32 ? launch_route<int32_t>(p, st) : launch_route<int64_t>(p, st);
 }

@@ -21,23 +21,32 @@
 
 namespace mx {
 
-// Scale of a block and the bracket of its reciprocal.  Below 2^-60 the values
-// and the scale are multiplied by 2^64 first (both exact), so that neither the
-// reciprocal nor the products leave the normal range.
+// Scale of a block and a bracket of its reciprocal.  s: FP64 holds the product
+// with 1/448 to 2^-53, and amax / 448 = (an 8-bit number) / 7 * 2^k has the
+// binary digits of sevenths, never within 2^-50 of the middle of two FP32
+// numbers, so rounding that product gives RN(amax / 448).  The bracket: the
+// approximate reciprocal is within one ulp, r_lo and r_up are 2 below and 12
+// above it, so that r_up exceeds 1/s by the 2^-21 that rounding the products
+// toward zero needs.  (Divisions and directed reciprocals in their place took
+// 40% of the kernel's instructions.)  Below 2^-60 the values and the scale are
+// multiplied by 2^64 first (both exact), so that neither the reciprocal nor
+// the products leave the normal range.
 struct B128Scale {
     float s;            // the scale as stored
     float ss;           // s times sc
-    float r_lo, r_hi;
+    float r_lo, r_up;
     float sc;
 };
 MX_DEVICE_INLINE B128Scale b128_scale(uint32_t amax_bits) {
     B128Scale b;
     const float amax = __uint_as_float(amax_bits << 16);
-    b.s = __fdiv_rn(amax, 448.0f);
+    b.s = (float)((double)amax * (1.0 / 448.0));
     b.sc = amax < 0x1p-60f ? 0x1p64f : 1.0f;
     b.ss = b.s * b.sc;
-    b.r_lo = amax_bits != 0u ? __frcp_rd(b.ss) : 0.0f;
-    b.r_hi = amax_bits != 0u ? __frcp_ru(b.ss) : 0.0f;
+    uint32_t r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=r"(r) : "f"(b.ss));
+    b.r_lo = amax_bits != 0u ? __uint_as_float(r - 2u) : 0.0f;
+    b.r_up = amax_bits != 0u ? __uint_as_float(r + 12u) : 0.0f;
     return b;
 }
 
@@ -50,7 +59,7 @@ MX_DEVICE_INLINE uint32_t b128_settle(uint32_t code, uint32_t diff, uint32_t w0,
         const uint32_t w = i < 2 ? w0 : w1;
         const float ax = fabsf((i & 1) ? bf16hi(w) : bf16lo(w)) * b.sc;
         const uint32_t c = (code >> (8 * i)) & 0x7Fu;   // the lower code, below 0x7E (448)
-        const float mid = 0.5f * ((c ? e4m3_pos_value(c) : 0.0f) + e4m3_pos_value(c + 1u));
+        const float mid = 0.5f * (e4m3_pos_value(c) + e4m3_pos_value(c + 1u));
         const float d = __fmaf_rn(-b.ss, mid, ax);
         if (d > 0.0f || (d == 0.0f && (c & 1u))) code += 1u << (8 * i);
     }
@@ -69,7 +78,12 @@ MX_DEVICE_INLINE uint4 b128_codes16(const uint4 &v0, const uint4 &v1, const B128
         for (int i = 0; i < 8; ++i) P[i] = mul2(P[i], SC);
     }
     float lo[16], hi[16];
-    bracket16(P, b.r_lo, b.r_hi, lo, hi);
+    const uint64_t RL = pk2(b.r_lo, b.r_lo), RU = pk2(b.r_up, b.r_up);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        upk2(mul2_rz(P[i], RL), lo[2 * i], lo[2 * i + 1]);
+        upk2(mul2_rz(P[i], RU), hi[2 * i], hi[2 * i + 1]);
+    }
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -84,10 +98,6 @@ MX_DEVICE_INLINE uint4 b128_codes16(const uint4 &v0, const uint4 &v1, const B128
 struct B128QuantParams {
     const uint16_t *src;
     int64_t ld;
-    int64_t src_rows;            // rows of src (a gather's indexes are checked against it)
-    const int32_t *row_index;    // nullable: source row of each output row
-    const int32_t *offsets;      // nullable: rows from offsets[groups] on are left as they are
-    int groups;
     int64_t M, K;
     uint8_t *codes;
     float *scales;
@@ -96,30 +106,24 @@ struct B128QuantParams {
 
 // One CTA per 128 x 128 tile, as quantize_kernel: 8 lanes per row, 16 elements
 // per lane and pass, all loads issued before the first use.
-template <bool TILE, bool GROUPED>
+template <bool TILE>
 __global__ void __launch_bounds__(kQThreads) quantize_b128_kernel(B128QuantParams p) {
     constexpr int kPasses = kQTileRows / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row0 = (int64_t)blockIdx.y * kQTileRows;
-    const int64_t kb = blockIdx.x;
+    const int64_t kb = blockIdx.x, band = blockIdx.y;
+    const int64_t row0 = band * kQTileRows;
     const int64_t col = kb * kQTileCols + (lane & 7) * 16;
     griddep_wait();
     griddep_launch_dependents();
-    int64_t live = p.M;
-    if (GROUPED) live = min((int64_t)max(p.offsets[p.groups], 0), p.M);
     uint4 v[kPasses][2];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int64_t row = row0 + i * 32 + warp * 4 + (lane >> 3);
         v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < live) {
-            int64_t from = row;
-            if (GROUPED && p.row_index != nullptr) from = p.row_index[row];
-            if (!GROUPED || (from >= 0 && from < p.src_rows)) {
-                const uint16_t *s = p.src + from * p.ld + col;
-                v[i][0] = ldg_stream(s);
-                v[i][1] = ldg_stream(s + 8);
-            }
+        if (row < p.M) {
+            const uint16_t *s = p.src + row * p.ld + col;
+            v[i][0] = ldg_stream(s);
+            v[i][1] = ldg_stream(s + 8);
         }
     }
     if (TILE) {
@@ -133,11 +137,11 @@ __global__ void __launch_bounds__(kQThreads) quantize_b128_kernel(B128QuantParam
 #pragma unroll
         for (int w = 0; w < kQThreads / 32; ++w) m = max(m, red[w]);
         const B128Scale b = b128_scale(m);
-        if (threadIdx.x == 0) p.scales[(int64_t)blockIdx.y * p.pitch + kb] = b.s;
+        if (threadIdx.x == 0) p.scales[band * p.pitch + kb] = b.s;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int64_t row = row0 + i * 32 + warp * 4 + (lane >> 3);
-            if (row < live) *reinterpret_cast<uint4 *>(p.codes + row * p.K + col) = b128_codes16(v[i][0], v[i][1], b);
+            if (row < p.M) *reinterpret_cast<uint4 *>(p.codes + row * p.K + col) = b128_codes16(v[i][0], v[i][1], b);
         }
     } else {
 #pragma unroll
@@ -148,9 +152,9 @@ __global__ void __launch_bounds__(kQThreads) quantize_b128_kernel(B128QuantParam
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
             const B128Scale b = b128_scale(m);
-            if (row < live) *reinterpret_cast<uint4 *>(p.codes + row * p.K + col) = b128_codes16(v[i][0], v[i][1], b);
-            // the scales' padding up to the pitch is 0 (a grouped call leaves rows past the last group alone)
-            if ((lane & 7) == 0 && row < (GROUPED ? live : p.pitch)) p.scales[kb * p.pitch + row] = b.s;
+            if (row < p.M) *reinterpret_cast<uint4 *>(p.codes + row * p.K + col) = b128_codes16(v[i][0], v[i][1], b);
+            // the scales' padding up to the pitch is 0
+            if ((lane & 7) == 0 && row < p.pitch) p.scales[kb * p.pitch + row] = b.s;
         }
     }
 }
@@ -185,80 +189,245 @@ __global__ void __launch_bounds__(256) dequantize_b128_kernel(const uint8_t *__r
     *reinterpret_cast<uint4 *>(dst + r * ld + c) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Quantize of rows grouped by expert into a format whose scales come in
-// 128-row tiles: each group begins a 128-row band of the scale buffer, so the
-// grouped GEMM's 128-row tiles read whole bands.  CTA (tile, band) finds its
-// group by a warp's walk and then quantizes 128 x 128 elements exactly as
-// quantize_kernel; bands past the last group's get zero scales.
+// Quantize of rows grouped by expert.  Formats whose scales come in 128-row
+// tiles: each group begins a 128-row band of the scale buffer, so the grouped
+// GEMM's 128-row tiles read whole bands; bands past the last group's get zero
+// scales.  A CTA takes one band (its group found by a warp) and p.slab K tiles
+// of 128 columns, the next tile's loads in flight while one is quantized, with
+// the arithmetic of the plain kernels.
+//
+// Order of the bands.  A gather of k choices per token reads every row k
+// times, and a source larger than L2 would come from HBM each time.  Within an
+// expert the rows are in the tokens' order, so bands at the same relative
+// place of their experts read neighbouring tokens: with `interleave` the CTAs
+// run through all experts side by side, in order of (band / bands of its
+// expert), and the rows' later reads are served by L2.
 struct GroupedQuantParams {
     const uint16_t *src;
     int64_t ld;
-    int64_t src_rows;
+    int64_t src_rows;            // indexes are checked against it
     const int32_t *row_index;    // nullable
     Groups groups;
     int64_t K;
     uint8_t *codes;
-    uint8_t *scales;
+    uint8_t *scales;             // 128-row tiles, or FP8_B128's floats
     int64_t sf_tiles_k;
+    int64_t pitch;               // FP8_B128: floats per K block
+    int slab, slabs;             // K tiles per CTA, CTAs per band
+    int interleave;
     const float *gscale;         // NVFP4: g
     float *gscale_out;           // NVFP4, nullable: receives g
 };
 
+// The band that CTA `i` of the interleaved order works on (warp-collective;
+// nb: shared memory for MAX groups).  With C(x) = sum over the groups of
+// floor(bands x / kSteps), the number of bands at relative places below x /
+// kSteps, the i-th band lies in the step with C(x - 1) <= i < C(x), found by
+// bisection, and is the (i - C(x - 1))-th of that step's bands in group order.
+// Each lane holds a run of consecutive groups.
+constexpr int kMaxGroups = 1024;
+struct Band {
+    int band, row0, row1;   // band of the scale buffer; rows
+};
+MX_DEVICE_INLINE Band interleaved_band(const Groups &g, int i, int *nb, int lane) {
+    constexpr int kSteps = 1024;
+    const int per = (g.count + 31) / 32, e0 = lane * per, e1 = min(e0 + per, g.count);
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) {
+        const int s = min(max(g.offsets[e], 0), g.rows), t = min(max(g.offsets[e + 1], 0), g.rows);
+        nb[e] = (max(t - s, 0) + 127) >> 7;
+        mine += nb[e];
+    }
+    __syncwarp();
+    const int total = (int)__reduce_add_sync(0xffffffffu, (unsigned)mine);
+    if (i >= total) return Band{i, 0, 0};
+    auto below = [&](int x) {   // this lane's part of C(x)
+        int c = 0;
+        for (int e = e0; e < e1; ++e) c += (int)((uint64_t)(uint32_t)nb[e] * (uint32_t)x / kSteps);
+        return c;
+    };
+    int lo = 0, hi = kSteps;   // C(lo) <= i < C(hi)
+    while (hi - lo > 1) {
+        const int x = (lo + hi) / 2;
+        if ((int)__reduce_add_sync(0xffffffffu, (unsigned)below(x)) <= i) lo = x;
+        else hi = x;
+    }
+    const int b0 = below(lo), d = below(hi) - b0;
+    int incl = d, bands = mine;   // inclusive prefixes over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, bands, o);
+        if (lane >= o) {
+            incl += u;
+            bands += v;
+        }
+    }
+    int k = i - (int)__reduce_add_sync(0xffffffffu, (unsigned)b0);
+    const int l = __ffs(__ballot_sync(0xffffffffu, incl > k)) - 1;
+    int band = 0, row0 = 0, row1 = 0;
+    if (lane == l) {
+        k -= incl - d;
+        band = bands - mine;
+        for (int e = e0; e < e1; ++e) {
+            const int a = (int)((uint64_t)(uint32_t)nb[e] * (uint32_t)lo / kSteps);
+            const int n = (int)((uint64_t)(uint32_t)nb[e] * (uint32_t)hi / kSteps) - a;
+            if (k < n) {
+                const int s = min(max(g.offsets[e], 0), g.rows), t = min(max(g.offsets[e + 1], 0), g.rows);
+                band += a + k;
+                row0 = s + (a + k) * 128;
+                row1 = min(t, row0 + 128);
+                break;
+            }
+            k -= n;
+            band += nb[e];
+        }
+    }
+    return Band{__shfl_sync(0xffffffffu, band, l), __shfl_sync(0xffffffffu, row0, l), __shfl_sync(0xffffffffu, row1, l)};
+}
+
+// Codes of 16 values (v0, v1) of row `row`, columns col .. col + 15, stored where
+// `ok`, and their block's scale byte, returned: the arithmetic of
+// quantize_seg16.  (A function of its own: shared with quantize_seg16, it made
+// the plain kernels 10% slower.)  A 32-element block spans lanes lane and
+// lane ^ 1, which call together.
 template <int FMT>
-__global__ void __launch_bounds__(kQThreads, quantize_min_blocks<FMT>()) quantize_grouped_kernel(GroupedQuantParams p) {
+MX_DEVICE_INLINE uint32_t quantize_codes16(const uint4 &v0, const uint4 &v1, int64_t row, bool ok, int64_t col,
+                                           int64_t K, const NvScale &ns, const NvTables *__restrict__ nvt,
+                                           uint8_t *__restrict__ codes) {
+    uint32_t m = absmax16(v0, v1);
+    if constexpr (FMT == FMT_NVFP4) {
+        const uint32_t sbyte = nv_block_scale(__uint_as_float(m << 16) * ns.sc, ns.g, ns.inv6g, nvt->val);
+        if (ok) {
+            uint32_t q0, q1;
+            const float r_lo = __fmul_rd(ns.rg_lo, nvt->inv_lo[sbyte]);
+            const float r_hi = __fmul_ru(ns.rg_hi, nvt->inv_hi[sbyte]);
+            nv_codes16(v0, v1, ns.g, nvt->val[sbyte], r_lo, r_hi, q0, q1, ns.sc);
+            *reinterpret_cast<uint2 *>(codes + row * (K / 2) + col / 2) = make_uint2(q0, q1);
+        }
+        return sbyte;
+    } else {
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const int E = mx_scale_byte<FMT, RULE_OCP>(m);
+        if (ok) {
+            const float inv = mx_inv_scale(E);
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[2 * e] = bf16lo(w[e]) * inv;
+                f[2 * e + 1] = bf16hi(w[e]) * inv;
+            }
+            store_mx_codes16<FMT>(codes, row, K, col, f);
+        }
+        return (uint32_t)E;
+    }
+}
+
+// CTAs per SM of the register allocation.
+template <int FMT>
+constexpr int grouped_min_blocks() {
+    return FMT == 6 ? 3 : 4;
+}
+constexpr int FMT_B128 = 6;
+
+template <int FMT>
+__global__ void __launch_bounds__(kQThreads, grouped_min_blocks<FMT>()) quantize_grouped_kernel(GroupedQuantParams p) {
     constexpr int kPasses = kQTileRows / 32;
-    __shared__ __align__(16) uint8_t sf_tile[quantize_sf_bytes<FMT>()];
     __shared__ NvTables nvt;
-    __shared__ int info[2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t col0 = (int64_t)blockIdx.x * kQTileCols;
-    const int cl = (lane & 7) * 16;
+    __shared__ int nb[kMaxGroups];
+    __shared__ Band info;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l8 = lane & 7;
+    const int bi = (int)(blockIdx.x / (unsigned)p.slabs);
+    const int tile0 = (int)(blockIdx.x - (unsigned)bi * (unsigned)p.slabs) * p.slab;
+    const int tiles = (int)((p.K + kQTileCols - 1) / kQTileCols);
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 0) {
-        GroupWalk walk(p.groups, 7, lane);
-        GroupBlock b;
-        int r0 = 0, r1 = 0;
-        if (walk.find((int)blockIdx.y, b)) {
-            r0 = b.start + ((int)blockIdx.y - b.first) * kQTileRows;
-            r1 = min(b.end, r0 + kQTileRows);
+        Band b{bi, 0, 0};
+        if (p.interleave) {
+            b = interleaved_band(p.groups, bi, nb, lane);
+        } else {
+            GroupWalk walk(p.groups, 7, lane);
+            GroupBlock g;
+            if (walk.find(bi, g)) {
+                b.row0 = g.start + (bi - g.first) * kQTileRows;
+                b.row1 = min(g.end, b.row0 + kQTileRows);
+            }
         }
-        if (lane == 0) {
-            info[0] = r0;
-            info[1] = r1;
-        }
+        if (lane == 0) info = b;
     }
     NvScale ns{1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
     if (FMT == FMT_NVFP4) {
         const float g = *p.gscale;
-        if (p.gscale_out != nullptr && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.gscale_out = g;
+        if (p.gscale_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.gscale_out = g;
         ns = nv_scale_setup(g);
         if (threadIdx.x < 128) nv_tables_fill(&nvt, threadIdx.x);
     }
     __syncthreads();
-    const int64_t row0 = info[0], row1 = info[1];
-    uint4 v[kPasses][2];
+    // from here on every warp runs by itself: its rows are 32 i + 4 warp .. + 3
+    // of the band, and its scale bytes go straight to their places
+    const int64_t band = info.band, row0 = info.row0, row1 = info.row1;
+    const int passes = (int)(row1 - row0 + 31) / 32;   // passes that hold rows
+    if (FMT == FMT_B128 && passes == 0) return;
+    int from[kPasses];   // this thread's source rows, -1 for none
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int64_t row = row0 + i * 32 + warp * 4 + (lane >> 3);
-        v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < row1 && col0 + cl < p.K) {
-            const int64_t from = p.row_index != nullptr ? p.row_index[row] : row;
-            if (from >= 0 && from < p.src_rows) {
-                const uint16_t *s = p.src + from * p.ld + col0 + cl;
+        from[i] = -1;
+        if (row < row1) {
+            const int64_t r = p.row_index != nullptr ? p.row_index[row] : row;
+            if (r >= 0 && r < p.src_rows) from[i] = (int)r;
+        }
+    }
+    const int tile1 = min(tile0 + p.slab, tiles);
+    for (int t = tile0; t < tile1; ++t) {
+        const int64_t col = (int64_t)t * kQTileCols + l8 * 16;
+        uint4 v[kPasses][2];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (from[i] >= 0 && col < p.K) {
+                const uint16_t *s = p.src + from[i] * p.ld + col;
                 v[i][0] = ldg_stream(s);
                 v[i][1] = ldg_stream(s + 8);
             }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        const int rl = i * 32 + warp * 4 + (lane >> 3);
-        quantize_seg16<FMT, RULE_OCP>(v[i][0], v[i][1], row0 + rl, row1, col0 + cl, p.K, col0, rl, cl, lane, ns, &nvt,
-                                      p.codes, sf_tile);
+        for (int i = 0; i < kPasses; ++i) {
+            const int rl = i * 32 + warp * 4 + (lane >> 3);
+            const int64_t row = row0 + rl;
+            const bool ok = row < row1 && col < p.K;
+            if constexpr (FMT == FMT_B128) {
+                if (i < passes) {
+                    uint32_t m = absmax16(v[i][0], v[i][1]);
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    const B128Scale b = b128_scale(m);
+                    if (ok) {
+                        *reinterpret_cast<uint4 *>(p.codes + row * p.K + col) = b128_codes16(v[i][0], v[i][1], b);
+                        if (l8 == 0) reinterpret_cast<float *>(p.scales)[t * p.pitch + row] = b.s;
+                    }
+                }
+            } else {
+                // the four scale bytes of a row in one 512-byte chunk (32-element
+                // blocks: all of the tile's; 16-element blocks: half of them)
+                constexpr bool k16 = FmtTraits<FMT>::kBlock == 16;
+                uint32_t w = 0u;
+                if (i < passes) {
+                    w = quantize_codes16<FMT>(v[i][0], v[i][1], row, ok, col, p.K, ns, &nvt, p.codes);
+                    w = ok && (k16 || (lane & 1) == 0) ? w << (8 * (k16 ? l8 & 3 : l8 >> 1)) : 0u;
+                    if (k16) w |= __shfl_xor_sync(0xffffffffu, w, 1);
+                    w |= __shfl_xor_sync(0xffffffffu, w, 2);
+                    if (!k16) w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                }
+                const int64_t chunk = k16 ? 2 * (int64_t)t + (l8 >> 2) : t;
+                if ((k16 ? l8 & 3 : l8) == 0 && chunk < p.sf_tiles_k)
+                    *reinterpret_cast<uint32_t *>(p.scales + (band * p.sf_tiles_k + chunk) * 512 + (rl & 31) * 16 +
+                                                  (rl >> 5) * 4) = w;
+            }
+        }
     }
-    __syncthreads();
-    store_sf_chunks<FMT>(sf_tile, p.scales, blockIdx.y, blockIdx.x, p.sf_tiles_k, threadIdx.x);
 }
 
 }  // namespace mx

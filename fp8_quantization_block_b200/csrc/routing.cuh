@@ -20,10 +20,15 @@
 
 namespace mx {
 
-constexpr int kRouteThreads = 1024;
+constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxGroups = 1024;
-constexpr int kRouteChunk = 8192;   // choices per CTA; up to this many, one CTA does it all
+// Choices per CTA: 2048 (one CTA alone up to there), more where that would make
+// over 128 CTAs, each of which adds up the counts of all the others.
+inline int64_t route_chunk(int64_t n) {
+    const int64_t per = (n + 127) / 128, unit = 32 * kRouteWarps;
+    return per <= 2048 ? 2048 : (per + unit - 1) / unit * unit;
+}
 
 struct RouteParams {
     const void *ids;          // int32 or int64 [n]
@@ -33,7 +38,8 @@ struct RouteParams {
     int32_t *offsets;         // [groups + 1]
     int32_t *row_token;       // [n]
     int32_t *slot;            // [n]
-    int32_t *counts;          // workspace: [groups][chunks], then their exclusive prefix sums
+    int32_t *counts;          // workspace: [chunks][groups]
+    int64_t chunk;
     int chunks;
 };
 
@@ -112,88 +118,109 @@ MX_DEVICE_INLINE void route_fill_tail(const RouteParams &p, int64_t live, int64_
     for (int64_t i = max(live, begin) + threadIdx.x; i < end; i += kRouteThreads) p.row_token[i] = -1;
 }
 
-// All of it in one CTA (n <= kRouteChunk).  Dynamic shared memory: 32 x groups ints.
+// Each warp's first slot of every expert, from the CTA's first slot of it
+// (first(g)) and the counts of the warps before.
+template <typename First>
+MX_DEVICE_INLINE void route_bases(int groups, int *cnt, First first) {
+    for (int g = threadIdx.x; g < groups; g += kRouteThreads) {
+        int base = first(g);
+#pragma unroll
+        for (int w = 0; w < kRouteWarps; ++w) {
+            const int c = cnt[w * groups + g];
+            cnt[w * groups + g] = base;
+            base += c;
+        }
+    }
+}
+MX_DEVICE_INLINE int route_cta_count(const int *cnt, int groups, int g) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWarps; ++w) sum += cnt[w * groups + g];
+    return sum;
+}
+
+// First slot of the experts 2 t and 2 t + 1 of thread t (groups <= 2 kRouteThreads)
+// from their totals; returns the number of slots.
+MX_DEVICE_INLINE int route_offsets(const RouteParams &p, int t0, int t1, int *warp_sums, int &o0, int &o1) {
+    int total;
+    o0 = block_exclusive(t0 + t1, warp_sums, total);
+    o1 = o0 + t0;
+    return total;
+}
+
+// All of it in one CTA.  Dynamic shared memory: kRouteWarps x groups ints.
 template <typename ID>
 __global__ void __launch_bounds__(kRouteThreads) route_small_kernel(RouteParams p) {
     extern __shared__ int cnt[];
     __shared__ int warp_sums[32];
+    __shared__ int first[kRouteMaxGroups];
     griddep_wait();
     griddep_launch_dependents();
     const int64_t per_warp = ((p.n + kRouteWarps - 1) / kRouteWarps + 31) / 32 * 32;
     route_count<ID>(p, 0, p.n, per_warp, cnt);
-    const int g = threadIdx.x;   // groups <= kRouteThreads
-    int sum = 0;
-    if (g < p.groups)
-        for (int w = 0; w < kRouteWarps; ++w) sum += cnt[w * p.groups + g];
-    int total;
-    int base = block_exclusive(sum, warp_sums, total);
-    if (g < p.groups) {
-        p.offsets[g] = base;
-        for (int w = 0; w < kRouteWarps; ++w) {
-            const int c = cnt[w * p.groups + g];
-            cnt[w * p.groups + g] = base;
-            base += c;
-        }
-    }
+    const int g0 = 2 * threadIdx.x, g1 = g0 + 1;
+    int o0, o1;
+    const int total = route_offsets(p, g0 < p.groups ? route_cta_count(cnt, p.groups, g0) : 0,
+                                    g1 < p.groups ? route_cta_count(cnt, p.groups, g1) : 0, warp_sums, o0, o1);
+    if (g0 < p.groups) p.offsets[g0] = first[g0] = o0;
+    if (g1 < p.groups) p.offsets[g1] = first[g1] = o1;
     if (threadIdx.x == 0) p.offsets[p.groups] = total;
+    __syncthreads();
+    route_bases(p.groups, cnt, [&](int g) { return first[g]; });
     __syncthreads();
     route_place<ID>(p, 0, p.n, per_warp, cnt);
     route_fill_tail(p, total, 0, p.n);
 }
 
-// Larger n: counts per chunk, one prefix sum over [groups][chunks], placing.
+// Larger n: counts per chunk, then every CTA adds up the counts of all chunks
+// (and of those before its own) and places its choices.
 template <typename ID>
 __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(RouteParams p) {
     extern __shared__ int cnt[];
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t begin = (int64_t)blockIdx.x * kRouteChunk, end = min(begin + kRouteChunk, p.n);
-    route_count<ID>(p, begin, end, kRouteChunk / kRouteWarps, cnt);
-    for (int g = threadIdx.x; g < p.groups; g += kRouteThreads) {
-        int sum = 0;
-        for (int w = 0; w < kRouteWarps; ++w) sum += cnt[w * p.groups + g];
-        p.counts[(int64_t)g * p.chunks + blockIdx.x] = sum;
-    }
-}
-
-static __global__ void __launch_bounds__(kRouteThreads) route_scan_kernel(RouteParams p) {
-    __shared__ int warp_sums[32];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t m = (int64_t)p.groups * p.chunks;
-    const int64_t per = (m + kRouteThreads - 1) / kRouteThreads;
-    const int64_t i0 = min((int64_t)threadIdx.x * per, m), i1 = min(i0 + per, m);
-    int sum = 0;
-    for (int64_t i = i0; i < i1; ++i) sum += p.counts[i];
-    int total;
-    int base = block_exclusive(sum, warp_sums, total);
-    for (int64_t i = i0; i < i1; ++i) {
-        const int c = p.counts[i];
-        p.counts[i] = base;
-        if (i % p.chunks == 0) p.offsets[i / p.chunks] = base;
-        base += c;
-    }
-    if (threadIdx.x == 0) p.offsets[p.groups] = total;
+    const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, p.n);
+    route_count<ID>(p, begin, end, p.chunk / kRouteWarps, cnt);
+    for (int g = threadIdx.x; g < p.groups; g += kRouteThreads)
+        p.counts[(int64_t)blockIdx.x * p.groups + g] = route_cta_count(cnt, p.groups, g);
 }
 
 template <typename ID>
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(RouteParams p) {
     extern __shared__ int cnt[];
-    griddep_wait();
+    __shared__ int warp_sums[32];
+    __shared__ int first[kRouteMaxGroups];
     griddep_launch_dependents();
-    const int64_t begin = (int64_t)blockIdx.x * kRouteChunk, end = min(begin + kRouteChunk, p.n);
-    route_count<ID>(p, begin, end, kRouteChunk / kRouteWarps, cnt);
-    for (int g = threadIdx.x; g < p.groups; g += kRouteThreads) {
-        int base = p.counts[(int64_t)g * p.chunks + blockIdx.x];
-        for (int w = 0; w < kRouteWarps; ++w) {
-            const int c = cnt[w * p.groups + g];
-            cnt[w * p.groups + g] = base;
-            base += c;
+    const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, p.n);
+    griddep_wait();   // the ids may come from the kernel before the counts
+    route_count<ID>(p, begin, end, p.chunk / kRouteWarps, cnt);
+    const int g0 = 2 * threadIdx.x, g1 = g0 + 1;
+    int all0 = 0, all1 = 0, before0 = 0, before1 = 0;
+#pragma unroll 8
+    for (int c = 0; c < p.chunks; ++c) {
+        const int32_t *row = p.counts + (int64_t)c * p.groups;
+        const int c0 = g0 < p.groups ? __ldg(row + g0) : 0, c1 = g1 < p.groups ? __ldg(row + g1) : 0;
+        all0 += c0;
+        all1 += c1;
+        if (c < (int)blockIdx.x) {
+            before0 += c0;
+            before1 += c1;
         }
     }
+    int o0, o1;
+    const int total = route_offsets(p, all0, all1, warp_sums, o0, o1);
+    if (g0 < p.groups) first[g0] = o0 + before0;
+    if (g1 < p.groups) first[g1] = o1 + before1;
+    if (blockIdx.x == 0) {
+        if (g0 < p.groups) p.offsets[g0] = o0;
+        if (g1 < p.groups) p.offsets[g1] = o1;
+        if (threadIdx.x == 0) p.offsets[p.groups] = total;
+    }
     __syncthreads();
-    route_place<ID>(p, begin, end, kRouteChunk / kRouteWarps, cnt);
-    route_fill_tail(p, p.offsets[p.groups], begin, end);
+    route_bases(p.groups, cnt, [&](int g) { return first[g]; });
+    __syncthreads();
+    route_place<ID>(p, begin, end, p.chunk / kRouteWarps, cnt);
+    route_fill_tail(p, total, begin, end);
 }
 
 struct CombineParams {

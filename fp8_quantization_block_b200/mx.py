@@ -12,6 +12,7 @@ torch tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -70,6 +71,8 @@ _lib = None
 
 def lib() -> ctypes.CDLL:
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -114,10 +117,13 @@ def lib() -> ctypes.CDLL:
 
 
 # ----------------------------------------------------------------- raw C names
+# sizes are pure functions of a few integers, asked for in every call
+@functools.lru_cache(maxsize=4096)
 def mx_codes_bytes(fmt: int, rows: int, cols: int) -> int:
     return int(lib().mx_codes_bytes(fmt, rows, cols))
 
 
+@functools.lru_cache(maxsize=4096)
 def mx_scales_bytes(fmt: int, rows: int, cols: int) -> int:
     return int(lib().mx_scales_bytes(fmt, rows, cols))
 
@@ -187,6 +193,7 @@ def split_units(tiles: int, workers: int, kt: int, mode: int, worker: int):
     return n_workers.value, [tuple(buf[5 * u:5 * u + 5]) for u in range(n)]
 
 
+@functools.lru_cache(maxsize=4096)
 def mx_route_workspace_bytes(tokens: int, choices: int, groups: int) -> int:
     return int(lib().mx_route_workspace_bytes(tokens, choices, groups))
 
@@ -197,6 +204,7 @@ def mx_route(ids_ptr, id_bits, tokens, choices, groups, offsets_ptr, row_token_p
                               ws_bytes, stream))
 
 
+@functools.lru_cache(maxsize=4096)
 def mx_grouped_scales_bytes(fmt: int, rows: int, groups: int, cols: int) -> int:
     return int(lib().mx_grouped_scales_bytes(fmt, rows, groups, cols))
 
@@ -244,8 +252,18 @@ def check(status: int, what: str = "libmx") -> None:
 
 # ----------------------------------------------------------------- torch helpers
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle: building a Stream object costs as much as the launch
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Is the tensor on another device than the current one?"""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError("CUDA tensors are wanted")
+    return at != torch._C._cuda_getDevice()
 
 
 def _ptr(t: torch.Tensor | None):
@@ -280,6 +298,9 @@ def empty(fmt: int, rows: int, cols: int, device="cuda") -> MxTensor:
 def quantize(x: torch.Tensor, fmt: int, gscale: torch.Tensor | None = None, out: MxTensor | None = None,
              stream=None) -> MxTensor:
     """bf16 [M, K] CUDA tensor (row pitch x.stride(0)) -> MxTensor."""
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return quantize(x, fmt, gscale, out, stream)
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     M, K = x.shape
     out = out if out is not None else empty(fmt, M, K, x.device)
@@ -326,12 +347,18 @@ def qsnr_sums(t: MxTensor, x: torch.Tensor, out: torch.Tensor | None = None, str
 
 
 def dequantize(t: MxTensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    if _elsewhere(t.codes):
+        with torch.cuda.device(t.codes.device):
+            return dequantize(t, out, stream)
     out = out if out is not None else torch.empty((t.rows, t.cols), dtype=torch.bfloat16, device=t.codes.device)
     check(mx_dequantize(t.c(), out.data_ptr(), out.stride(0), _stream(stream)), "mx_dequantize")
     return out
 
 
 def gemm(A: MxTensor, B: MxTensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    if _elsewhere(A.codes):
+        with torch.cuda.device(A.codes.device):
+            return gemm(A, B, out, stream)
     out = out if out is not None else torch.empty((A.rows, B.rows), dtype=torch.bfloat16, device=A.codes.device)
     check(mx_gemm(A.c(), B.c(), out.data_ptr(), out.stride(0), _stream(stream)), "mx_gemm")
     return out
@@ -383,32 +410,14 @@ def _rows_ok(x: torch.Tensor, what: str) -> None:
 
 def _pitch(x: torch.Tensor) -> int:
     """Row pitch of a matrix (a single row's stride says nothing)."""
-    return x.stride(0) if x.shape[0] > 1 else max(x.shape[1], x.stride(0) // 8 * 8)
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
 def _same_device(first: torch.Tensor, *others) -> None:
+    at = first.get_device()
     for t in others:
-        _need(t is None or t.device == first.device, "all tensors on one device are wanted")
-
-
-class _On:
-    """The device of a call's tensors made current around it, where it is another than the current one."""
-    __slots__ = ("back", "stream")
-
-    def __init__(self, t: torch.Tensor, stream):
-        _need(t.is_cuda, "CUDA tensors are wanted")
-        dev, now = t.device.index, torch.cuda.current_device()
-        self.back = now if now != dev else -1
-        if self.back >= 0:
-            torch.cuda.set_device(dev)
-        self.stream = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
-
-    def __enter__(self):
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.back >= 0:
-            torch.cuda.set_device(self.back)
+        if t is not None and t.get_device() != at:
+            raise ValueError("all tensors on one device are wanted")
 
 
 def _groups(offsets: torch.Tensor) -> MxGroupsC:
@@ -421,20 +430,23 @@ def route(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = None
     """Expert ids [tokens, choices] (int32 or int64; others than 0 .. experts - 1 have no slot) -> Routing."""
     _need(ids.dtype in (torch.int32, torch.int64) and ids.dim() == 2 and ids.is_contiguous(),
           "ids: a contiguous int32 or int64 matrix is wanted")
+    if _elsewhere(ids):
+        with torch.cuda.device(ids.device):
+            return route(ids, experts, workspace, stream)
     tokens, choices = ids.shape
     n, dev = tokens * choices, ids.device
-    with _On(ids, stream) as st:
-        both = torch.empty(experts + 1 + 2 * n, dtype=torch.int32, device=dev)
-        r = Routing(both[:experts + 1], both[experts + 1:experts + 1 + n], both[experts + 1 + n:].view(tokens, choices))
-        need = mx_route_workspace_bytes(tokens, choices, experts)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _same_device(ids, workspace)
-        at = both.data_ptr()
-        check(mx_route(ids.data_ptr(), 32 if ids.dtype == torch.int32 else 64, tokens, choices, experts, at,
-                       at + 4 * (experts + 1), at + 4 * (experts + 1 + n), _ptr(workspace),
-                       0 if workspace is None else workspace.numel() * workspace.element_size(), st), "mx_route")
-    return r
+    _need(choices >= 1 and 1 <= experts <= MX_MAX_GROUPS, "at least one choice and 1 to MX_MAX_GROUPS experts are wanted")
+    _same_device(ids, workspace)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+    row_token = torch.empty(n, dtype=torch.int32, device=dev)
+    slot = torch.empty((tokens, choices), dtype=torch.int32, device=dev)
+    need = mx_route_workspace_bytes(tokens, choices, experts)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    check(mx_route(ids.data_ptr(), 32 if ids.dtype == torch.int32 else 64, tokens, choices, experts, offsets.data_ptr(),
+                   row_token.data_ptr(), slot.data_ptr(), _ptr(workspace),
+                   0 if workspace is None else _nbytes(workspace), _stream(stream)), "mx_route")
+    return Routing(offsets, row_token, slot)
 
 
 def empty_grouped(fmt: int, rows: int, groups: int, cols: int, device="cuda") -> MxTensor:
@@ -454,6 +466,9 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, row_index
     """Rows of x (x[row_index[t]], or x itself) quantized for gemm_grouped.  NVFP4 wants gscale (g)."""
     _rows_ok(x, "x")
     groups = _groups(offsets)
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return quantize_grouped(x, offsets, fmt, row_index, gscale, out, stream)
     K = x.shape[1]
     if row_index is not None:
         _need(row_index.dtype == torch.int32 and row_index.dim() == 1 and row_index.is_contiguous(),
@@ -466,25 +481,27 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, row_index
         _need(_nbytes(out.codes) >= mx_codes_bytes(fmt, rows, K) and
               _nbytes(out.scales) >= mx_grouped_scales_bytes(fmt, rows, groups.count, K), "out: a buffer is too small")
     _same_device(x, offsets, row_index, gscale, out.codes, out.scales, out.gscale)
-    with _On(x, stream) as st:
-        check(mx_quantize_grouped(fmt, x.data_ptr(), x.shape[0], K, _pitch(x), _ptr(row_index), groups, out.c(),
-                                  _ptr(gscale), st), "mx_quantize_grouped")
+    check(mx_quantize_grouped(fmt, x.data_ptr(), x.shape[0], K, _pitch(x), _ptr(row_index), groups, out.c(), _ptr(gscale),
+                              _stream(stream)), "mx_quantize_grouped")
     return out
 
 
 def quantize_experts(w: torch.Tensor, fmt: int, stream=None) -> MxTensor:
     """bf16 [experts, N, K] -> the experts' matrices one after another, as gemm_grouped takes them for B (rows N)."""
     _need(w.dtype == torch.bfloat16 and w.dim() == 3 and w.stride(2) == 1, "w: bf16 [experts, N, K] is wanted")
+    if _elsewhere(w):
+        with torch.cuda.device(w.device):
+            return quantize_experts(w, fmt, stream)
     E, N, K = w.shape
     cb, sb = mx_codes_bytes(fmt, N, K), mx_scales_bytes(fmt, N, K)
     codes = torch.empty(max(E * cb, 1), dtype=torch.uint8, device=w.device)
     scales = torch.empty(max(E * sb, 1), dtype=torch.uint8, device=w.device)
     g = torch.empty(E, dtype=torch.float32, device=w.device) if fmt == MX_NVFP4 else None
-    with _On(w, stream) as st:
-        for e in range(E):
-            one = MxTensorC(fmt, 0, N, K, codes.data_ptr() + e * cb, scales.data_ptr() + e * sb,
-                            None if g is None else g.data_ptr() + 4 * e)
-            check(mx_quantize(fmt, w[e].data_ptr(), N, K, _pitch(w[e]), one, None, st), "mx_quantize")
+    st = _stream(stream)
+    for e in range(E):
+        one = MxTensorC(fmt, 0, N, K, codes.data_ptr() + e * cb, scales.data_ptr() + e * sb,
+                        None if g is None else g.data_ptr() + 4 * e)
+        check(mx_quantize(fmt, w[e].data_ptr(), N, K, _pitch(w[e]), one, None, st), "mx_quantize")
     return MxTensor(fmt, N, K, codes, scales, g)
 
 
@@ -493,6 +510,9 @@ def gemm_grouped(A: MxTensor, B: MxTensor, offsets: torch.Tensor, out: torch.Ten
     """C[t] = f(A[t] B_g^T) for the rows t of every group g; B as quantize_experts gives it.  bf16 [A.rows, B.rows],
     rows of no group left as they are."""
     groups = _groups(offsets)
+    if _elsewhere(A.codes):
+        with torch.cuda.device(A.codes.device):
+            return gemm_grouped(A, B, offsets, out, epilogue, stream)
     E = groups.count
     _need(_nbytes(A.codes) >= mx_codes_bytes(A.fmt, A.rows, A.cols) and
           _nbytes(A.scales) >= mx_grouped_scales_bytes(A.fmt, A.rows, E, A.cols), "A: a buffer is too small")
@@ -505,9 +525,8 @@ def gemm_grouped(A: MxTensor, B: MxTensor, offsets: torch.Tensor, out: torch.Ten
         _rows_ok(out, "out")
         _need(out.shape == (A.rows, B.rows), "out: another size")
     _same_device(A.codes, A.scales, A.gscale, B.codes, B.scales, B.gscale, offsets, out)
-    with _On(A.codes, stream) as st:
-        check(mx_gemm_grouped(A.c(), B.c(), groups, out.data_ptr(), max(out.stride(0), B.rows) if A.rows == 1 else out.stride(0),
-                              epilogue, st), "mx_gemm_grouped")
+    check(mx_gemm_grouped(A.c(), B.c(), groups, out.data_ptr(), _pitch(out), epilogue, _stream(stream)),
+          "mx_gemm_grouped")
     return out
 
 
@@ -518,17 +537,19 @@ def combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, out: tor
     _need(slot.dtype == torch.int32 and slot.dim() == 2 and slot.is_contiguous(), "slot: a contiguous int32 matrix is wanted")
     _need(weights.dtype == torch.float32 and weights.shape == slot.shape and weights.is_contiguous(),
           "weights: a contiguous float32 matrix of slot's shape is wanted")
+    if _elsewhere(y):
+        with torch.cuda.device(y.device):
+            return combine(y, slot, weights, out, stream)
     tokens, choices = slot.shape
+    rows, cols = y.shape
     if out is None:
-        out = torch.empty((tokens, y.shape[1]), dtype=torch.bfloat16, device=y.device)
+        out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=y.device)
     else:
         _rows_ok(out, "out")
-        _need(out.shape == (tokens, y.shape[1]), "out: another size")
+        _need(out.shape == (tokens, cols), "out: another size")
     _same_device(y, slot, weights, out)
-    with _On(y, stream) as st:
-        check(mx_combine(y.data_ptr(), y.shape[0], y.shape[1], max(y.stride(0), y.shape[1]), slot.data_ptr(),
-                         weights.data_ptr(), tokens, choices, out.data_ptr(), max(out.stride(0), y.shape[1]), st),
-              "mx_combine")
+    check(mx_combine(y.data_ptr(), rows, cols, y.stride(0) if rows > 1 else cols, slot.data_ptr(), weights.data_ptr(),
+                     tokens, choices, out.data_ptr(), out.stride(0) if tokens > 1 else cols, _stream(stream)), "mx_combine")
     return out
 
 

@@ -341,7 +341,7 @@ typedef struct {
  *   slot      [tokens * choices] the slot of each choice, -1 for an id outside
  *             [0, groups) (a padded or dropped choice).
  * The same expert twice in a token gives two slots.  workspace: device, 4-byte
- * aligned, mx_route_workspace_bytes bytes (0 for up to 8192 choices: NULL will
+ * aligned, mx_route_workspace_bytes bytes (0 for up to 2048 choices: NULL will
  * do); scratch, not to be shared by calls that overlap on the GPU.
  * groups <= MX_MAX_GROUPS, tokens * choices < 2^31. */
 size_t mx_route_workspace_bytes(int64_t tokens, int choices, int groups);

@@ -32,8 +32,8 @@ def test_sizes():
     assert mx.mx_grouped_scales_bytes(0, 300, 4, 256) == (300 + 127 * 4) // 128 * 128 * 8
     assert mx.mx_grouped_scales_bytes(0, 3, 100, 256) == 3 * 128 * 8               # at most a band per row
     assert mx.mx_grouped_scales_bytes(8, 3, 1, 256) == 0 and mx.mx_grouped_scales_bytes(5, 3, 1, 256) == 0
-    assert mx.mx_route_workspace_bytes(1024, 8, 64) == 0
-    assert mx.mx_route_workspace_bytes(1025, 8, 64) == 2 * 64 * 4
+    assert mx.mx_route_workspace_bytes(256, 8, 64) == 0
+    assert mx.mx_route_workspace_bytes(257, 8, 64) == 2 * 64 * 4
     assert mx.mx_route_workspace_bytes(2 ** 31, 2, 4) == 0
     assert ctypes.sizeof(mx.MxGroupsC) == 16
     assert mx.MX_MAX_GROUPS == 1024
