@@ -252,6 +252,14 @@ __global__ void __launch_bounds__(kB128Threads, 1)
             B128Tile t;
             for (int i = worker; !stop && tiles.at(i, t); i += workers) {
                 const int a_row = t.row0 + (PAIR ? 128 * (int)rank : 0);
+                // GROUPED: of A only the 32-row boxes that hold rows of the group
+                // (each CTA's own; the leader's barrier expects both CTAs')
+                const int rows = t.row_end - t.row0;
+                const int boxes0 = GROUPED ? min(p.a_bytes / (32 * kStageKBytes), (rows + 31) / 32) : 0;
+                const int boxes1 = GROUPED && PAIR ? min(4, max(rows - 128 + 31, 0) / 32) : 0;
+                const int boxes = rank == 0 ? boxes0 : boxes1;
+                const uint32_t tx = GROUPED ? (uint32_t)((boxes0 + boxes1) * 32 * kStageKBytes + (PAIR ? 2 : 1) * p.b_bytes)
+                                            : (uint32_t)((PAIR ? 2 : 1) * (p.a_bytes + p.b_bytes));
                 const int b_row = t.group * p.N + t.n0 + (PAIR ? (p.bn / 2) * (int)rank : 0);
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!mbar_wait_at(empty0 + 8u * (uint32_t)s, ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
@@ -261,12 +269,22 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     if (lane == 0) {
                         if (PAIR) {
                             const uint32_t bar = full_leader0 + 8u * (uint32_t)s;
-                            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)(p.a_bytes + p.b_bytes));
-                            tma_load_2d_pair(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, a_row, bar);
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
+                            if (GROUPED)
+                                for (int b = 0; b < boxes; ++b)
+                                    tma_load_2d_pair(smem_a + s * p.a_bytes + b * 32 * kStageKBytes, &tmA,
+                                                     kb * kStageKBytes, a_row + 32 * b, bar);
+                            else
+                                tma_load_2d_pair(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, a_row, bar);
                             tma_load_2d_pair(smem_b + s * p.b_bytes, &tmB, kb * kStageKBytes, b_row, bar);
                         } else {
-                            mbar_arrive_expect_tx(&full[s], (uint32_t)(p.a_bytes + p.b_bytes));
-                            tma_load_2d(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, a_row, &full[s]);
+                            mbar_arrive_expect_tx(&full[s], tx);
+                            if (GROUPED)
+                                for (int b = 0; b < boxes; ++b)
+                                    tma_load_2d(smem_a + s * p.a_bytes + b * 32 * kStageKBytes, &tmA, kb * kStageKBytes,
+                                                a_row + 32 * b, &full[s]);
+                            else
+                                tma_load_2d(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, a_row, &full[s]);
                             tma_load_2d(smem_b + s * p.b_bytes, &tmB, kb * kStageKBytes, b_row, &full[s]);
                         }
                     }

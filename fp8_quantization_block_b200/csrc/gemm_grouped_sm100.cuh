@@ -20,7 +20,8 @@ template <int FMT, int STAGES>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmSfa,
-                        const __grid_constant__ CUtensorMap tmSfb, GemmParams p, const Groups groups) {
+                        const __grid_constant__ CUtensorMap tmSfb, GemmParams p, const Groups groups, const uint32_t a_box_tx) {
+    // a_box_tx (run-time types): bytes a 32-row box of A reports; p.stage_tx is B's
     constexpr int BN = 256;
     using F = GemmFmt<FMT>;
     using L = GemmSmem<FMT, BN, STAGES>;
@@ -102,15 +103,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             bool stop = false;
             for (int u = 0; u < n_units && !stop; ++u) {
                 const Tile t = tile_at(u);
+                // of A's 128 rows only the 32-row boxes that hold rows of the
+                // group: what a tile brings from L2, whose rate to the SMs
+                // bounds the ragged sizes
+                const int boxes = min(4, (t.row_end - t.row0 + 31) / 32);
+                const uint32_t tx = FMT == kGemmRuntimeTypes ? p.stage_tx + (uint32_t)boxes * a_box_tx
+                                                             : (uint32_t)(boxes * 32 * kStageKBytes + L::kBBytes);
                 for (int kt = 0; kt < p.num_kt; ++kt) {
                     if (!mbar_wait_bounded(&empty[s], ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
                         stop = true;
                         break;
                     }
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&full[s], FMT == kGemmRuntimeTypes ? p.stage_tx
-                                                                                 : (uint32_t)(L::kABytes + L::kBBytes));
-                        tma_load_2d(smem + L::kOffA + s * L::kABytes, &tmA, kt * kStageKBytes, t.row0, &full[s]);
+                        mbar_arrive_expect_tx(&full[s], tx);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(smem + L::kOffA + s * L::kABytes + b * 32 * kStageKBytes, &tmA,
+                                        kt * kStageKBytes, t.row0 + 32 * b, &full[s]);
                         tma_load_2d(smem + L::kOffB + s * L::kBBytes, &tmB, kt * kStageKBytes, t.group * p.N + t.n0,
                                     &full[s]);
                     }

@@ -107,7 +107,7 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     if (p.stages > kB128MaxStages) p.stages = kB128MaxStages;
     const size_t smem = (size_t)fixed + (size_t)p.stages * (p.a_bytes + p.b_bytes);
     CUtensorMap ta, tb;
-    if (!make_tmap_u8(&ta, A->codes, M, K, a_rows)) return MX_ERR_CUDA;
+    if (!make_tmap_u8(&ta, A->codes, M, K, groups ? 32 : a_rows)) return MX_ERR_CUDA;
     if (!make_tmap_u8(&tb, B->codes, G * N, K, b_rows)) return MX_ERR_CUDA;
     p.sa = reinterpret_cast<const float *>(A->scales);
     p.sb = reinterpret_cast<const float *>(B->scales);
@@ -159,10 +159,10 @@ mx_status launch_grouped_t(const mx_tensor *A, const mx_tensor *B, const mx_grou
     const int64_t bands = group_bands(M, G);
     CUtensorMap ta, tb, tc, tsa, tsb;
     if (FMT == kGemmRuntimeTypes) {
-        if (!make_tmap_codes_f8f6f4(&ta, A->fmt, A->codes, M, K, kBM)) return MX_ERR_CUDA;
+        if (!make_tmap_codes_f8f6f4(&ta, A->fmt, A->codes, M, K, 32)) return MX_ERR_CUDA;
         if (!make_tmap_codes_f8f6f4(&tb, B->fmt, B->codes, G * N, K, BN)) return MX_ERR_CUDA;
     } else {
-        if (!make_tmap_u8(&ta, A->codes, M, kbytes, kBM)) return MX_ERR_CUDA;
+        if (!make_tmap_u8(&ta, A->codes, M, kbytes, 32)) return MX_ERR_CUDA;
         if (!make_tmap_u8(&tb, B->codes, G * N, kbytes, BN)) return MX_ERR_CUDA;
     }
     if (!make_tmap_sf(&tsa, A->scales, bands, sf_tiles_k, kSfGroup * GemmFmt<FMT>::kChunks, 1)) return MX_ERR_CUDA;
@@ -188,7 +188,7 @@ mx_status launch_grouped_t(const mx_tensor *A, const mx_tensor *B, const mx_grou
     p.use_tma_store = tma_store ? 1 : 0;
     p.skip_producer = g_skip_producer.load();
     p.ab_types = (f8f6f4_type(A->fmt) << 7) | (f8f6f4_type(B->fmt) << 10);
-    p.stage_tx = (uint32_t)(kStageKBytes * (kBM * fmt_bits(A->fmt) + BN * fmt_bits(B->fmt)) / 8);
+    p.stage_tx = (uint32_t)(kStageKBytes * BN * fmt_bits(B->fmt) / 8);
     p.wait_limit_ns = g_wait_limit_ns.load();
     const int64_t tiles = bands * p.n_blocks;
     if (tiles > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
@@ -197,7 +197,8 @@ mx_status launch_grouped_t(const mx_tensor *A, const mx_tensor *B, const mx_grou
     if (grid > tiles) grid = tiles;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)grid, 1, 1), kGemmThreads, L::kAlloc, st, attr);
-    cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, tsa, tsb, p, Groups{groups->offsets, groups->count, (int)M});
+    cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, tsa, tsb, p, Groups{groups->offsets, groups->count, (int)M},
+                       (uint32_t)(kStageKBytes * 32 * fmt_bits(A->fmt) / 8));
     return last_launch();
 }
 
