@@ -6,12 +6,20 @@
 //   element q = RNE_e4m3(x / s) of the exact quotient, saturating at 448; a
 //           block of zeros has s = 0 and the signed zeros of x.
 //
-// A quotient of a bf16 value and an FP32 scale often lies next to the middle
-// of two codes (x and max|x| are short numbers, and s is max|x| / 448 but for
-// one rounding), so rounding the quotient to FP32 first would change codes.
-// As for NVFP4, two products with 1/s rounded down and up bracket it, both
-// cast; where their codes differ the sign of |x| - s * middle, exact in one
-// fma, decides.
+// Rounding the exact quotient needs no division.  Write Q = 448 x / max|x|, so
+// that x / s = Q (1 + d), |d| <= 2^-24 from the rounding of s.  x and max|x| are
+// bf16, 8-bit numbers X 2^i and A 2^j, and the middle m of two E4M3 codes is an
+// odd number o <= 31 times a power of two, so Q against m compares 7 X 2^k with
+// A o, integers of which the second is at most 255 * 31: they are equal or at
+// least 1/7905 > 2^-13 apart, relatively.  Hence
+//   - Q next to no middle: any value within 2^-13.3 of Q rounds to the code;
+//   - Q on a middle: x / s lies on the side that s was rounded away from
+//     (above where s < max|x| / 448, below where s is above), or is a tie.
+// So x is multiplied with 1/s moved by 512 ulps (2^-15 to 2^-14) to that side,
+// or not at all where s is exact, and always by 4 more, over the reciprocal's
+// and the product's errors; cutting the product to 16 bits then gives an exact
+// tie back (and leaves the moved products on their side), and the cast to E4M3
+// does the rest.  All of it changes a product by less than 2^-13.4.
 //
 // Bound by HBM: 2 bytes read and 1 written per element (+ 4/128 per row block).
 #pragma once
@@ -21,76 +29,59 @@
 
 namespace mx {
 
-// Scale of a block and a bracket of its reciprocal.  s: FP64 holds the product
-// with 1/448 to 2^-53, and amax / 448 = (an 8-bit number) / 7 * 2^k has the
-// binary digits of sevenths, never within 2^-50 of the middle of two FP32
-// numbers, so rounding that product gives RN(amax / 448).  The bracket: the
-// approximate reciprocal is within one ulp, r_lo and r_up are 2 below and 12
-// above it, so that r_up exceeds 1/s by the 2^-21 that rounding the products
-// toward zero needs.  (Divisions and directed reciprocals in their place took
-// 40% of the kernel's instructions.)  Below 2^-60 the values and the scale are
-// multiplied by 2^64 first (both exact), so that neither the reciprocal nor
-// the products leave the normal range.
+// Scale of a block and the factor of its values, 1/s moved as above.  s: FP64
+// holds the product with 1/448 to 2^-53, and max|x| / 448 = (an 8-bit number) /
+// 7 * 2^k has the binary digits of sevenths, never within 2^-50 of the middle of
+// two FP32 numbers, so rounding that product gives RN(max|x| / 448); the sign
+// of max|x| - 448 s is exact in one fma.  (With a division, directed
+// reciprocals and two casts of a bracket per value in their place, 28600 x 8192
+// took 161 us instead of 106.)
 struct B128Scale {
-    float s;            // the scale as stored
-    float ss;           // s times sc
-    float r_lo, r_up;
-    float sc;
+    float s;      // the scale as stored
+    float r;      // the factor
+    bool small;   // a subnormal s, or nearly: the quotients are divided out
 };
 MX_DEVICE_INLINE B128Scale b128_scale(uint32_t amax_bits) {
     B128Scale b;
     const float amax = __uint_as_float(amax_bits << 16);
     b.s = (float)((double)amax * (1.0 / 448.0));
-    b.sc = amax < 0x1p-60f ? 0x1p64f : 1.0f;
-    b.ss = b.s * b.sc;
+    const float e = __fmaf_rn(-448.0f, b.s, amax);
     uint32_t r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=r"(r) : "f"(b.ss));
-    b.r_lo = amax_bits != 0u ? __uint_as_float(r - 2u) : 0.0f;
-    b.r_up = amax_bits != 0u ? __uint_as_float(r + 12u) : 0.0f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=r"(r) : "f"(b.s));
+    r += e > 0.0f ? 516u : (e < 0.0f ? (uint32_t)-508 : 4u);
+    b.r = amax_bits != 0u ? __uint_as_float(r) : 0.0f;
+    b.small = amax_bits != 0u && amax < 0x1p-60f;
     return b;
 }
 
-// Settle the bytes of a word of four codes whose bracket straddles a middle:
-// diff is nonzero in those bytes; w0, w1 hold the four bf16 inputs.
-MX_DEVICE_INLINE uint32_t b128_settle(uint32_t code, uint32_t diff, uint32_t w0, uint32_t w1, const B128Scale &b) {
-    while (diff != 0u) {
-        const int i = (__ffs(diff) - 1) >> 3;
-        diff &= ~(0xFFu << (8 * i));
-        const uint32_t w = i < 2 ? w0 : w1;
-        const float ax = fabsf((i & 1) ? bf16hi(w) : bf16lo(w)) * b.sc;
-        const uint32_t c = (code >> (8 * i)) & 0x7Fu;   // the lower code, below 0x7E (448)
-        const float mid = 0.5f * (e4m3_pos_value(c) + e4m3_pos_value(c + 1u));
-        const float d = __fmaf_rn(-b.ss, mid, ax);
-        if (d > 0.0f || (d == 0.0f && (c & 1u))) code += 1u << (8 * i);
-    }
-    return code;
+// x / s for the cast, exactly: the FP64 quotient (x and s hold 32 bits between
+// them and a middle 5, so it is on its side of every middle) rounded to odd.
+MX_DEVICE_INLINE float b128_divide(float x, float s) {
+    const double q = (double)x / (double)s;
+    const float f = __double2float_rz(q);
+    return (double)f == q ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
 // E4M3 codes of 16 bf16 values under one scale.
 MX_DEVICE_INLINE uint4 b128_codes16(const uint4 &v0, const uint4 &v1, const B128Scale &b) {
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    uint64_t P[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) P[i] = pk2(bf16lo(w[i]), bf16hi(w[i]));
-    if (b.sc != 1.0f) {
-        const uint64_t SC = pk2(b.sc, b.sc);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) P[i] = mul2(P[i], SC);
-    }
-    float lo[16], hi[16];
-    const uint64_t RL = pk2(b.r_lo, b.r_lo), RU = pk2(b.r_up, b.r_up);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        upk2(mul2_rz(P[i], RL), lo[2 * i], lo[2 * i + 1]);
-        upk2(mul2_rz(P[i], RU), hi[2 * i], hi[2 * i + 1]);
-    }
     uint32_t c[4];
+    if (!b.small) {
+        const uint64_t R = pk2(b.r, b.r);
+        float f[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        c[i] = cvt4_fp8<FMT_E4M3>(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-        const uint32_t h = cvt4_fp8<FMT_E4M3>(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-        const uint32_t d = (c[i] ^ h) & 0x7F7F7F7Fu;
-        if (d != 0u) c[i] = b128_settle(c[i], d, w[2 * i], w[2 * i + 1], b);
+        for (int i = 0; i < 8; ++i) {
+            upk2(mul2(pk2(bf16lo(w[i]), bf16hi(w[i])), R), f[2 * i], f[2 * i + 1]);
+            f[2 * i] = __uint_as_float(__float_as_uint(f[2 * i]) & 0xFFFFFF00u);
+            f[2 * i + 1] = __uint_as_float(__float_as_uint(f[2 * i + 1]) & 0xFFFFFF00u);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = cvt4_fp8<FMT_E4M3>(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = cvt4_fp8<FMT_E4M3>(b128_divide(bf16lo(w[2 * i]), b.s), b128_divide(bf16hi(w[2 * i]), b.s),
+                                      b128_divide(bf16lo(w[2 * i + 1]), b.s), b128_divide(bf16hi(w[2 * i + 1]), b.s));
     }
     return make_uint4(c[0], c[1], c[2], c[3]);
 }
@@ -107,7 +98,7 @@ struct B128QuantParams {
 // One CTA per 128 x 128 tile, as quantize_kernel: 8 lanes per row, 16 elements
 // per lane and pass, all loads issued before the first use.
 template <bool TILE>
-__global__ void __launch_bounds__(kQThreads) quantize_b128_kernel(B128QuantParams p) {
+__global__ void __launch_bounds__(kQThreads, 4) quantize_b128_kernel(B128QuantParams p) {
     constexpr int kPasses = kQTileRows / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t kb = blockIdx.x, band = blockIdx.y;
@@ -323,15 +314,10 @@ MX_DEVICE_INLINE uint32_t quantize_codes16(const uint4 &v0, const uint4 &v1, int
     }
 }
 
-// CTAs per SM of the register allocation.
-template <int FMT>
-constexpr int grouped_min_blocks() {
-    return FMT == 6 ? 3 : 4;
-}
 constexpr int FMT_B128 = 6;
 
 template <int FMT>
-__global__ void __launch_bounds__(kQThreads, grouped_min_blocks<FMT>()) quantize_grouped_kernel(GroupedQuantParams p) {
+__global__ void __launch_bounds__(kQThreads, 4) quantize_grouped_kernel(GroupedQuantParams p) {
     constexpr int kPasses = kQTileRows / 32;
     __shared__ NvTables nvt;
     __shared__ int nb[kMaxGroups];

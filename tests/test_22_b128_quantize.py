@@ -80,3 +80,19 @@ def test_round_trip_of_representable_blocks():
     x[2] *= -(2.0 ** -20)
     x = x.bfloat16().cuda()
     assert torch.equal(mx.dequantize(mx.quantize(x, mx.MX_FP8_B128)), x)
+
+
+def test_every_pair_of_mantissas():
+    """All 128 x 128 pairs of a block's largest and another element's mantissa, at every distance of exponents that
+    reaches a nonzero code: among them every tie and everything next to one."""
+    rows = []
+    for top in range(128, 256):
+        others = torch.tensor([[m * 2.0 ** -k for k in range(0, 21)] for m in range(128, 256)]).reshape(-1)
+        others = others[others <= top]
+        others = torch.where(torch.arange(others.numel()) % 2 == 0, others, -others)
+        pad = torch.zeros(-others.numel() % 127)
+        block = torch.cat((others, pad)).view(-1, 127)
+        rows.append(torch.cat((torch.full((block.shape[0], 1), float(top)), block), 1))
+    x = torch.cat(rows)
+    for scale in (1.0, 2.0 ** -60, 2.0 ** -75, 2.0 ** 100):
+        check((x * scale).bfloat16().cuda(), mx.MX_FP8_B128, 1)
