@@ -29,11 +29,11 @@
 // Registers move from warps 0-3 to the drain warps (setmaxnreg), whose sums
 // take 128 of them each for 256-column tiles.
 //
-// Tile sizes are run-time numbers: bm rows (32, 64, 128, or 256 on a CTA pair)
-// and bn columns (a multiple of 32 up to 256), so that few-row products, which
-// are bound by the weight stream, spread over all SMs.  PAIR: two CTAs share a
-// 256 x bn tile with cta_group::2 MMAs, each loading its own 128 rows of A and
-// half of B: per SM half the B traffic for the same MMAs.
+// Tile sizes are run-time numbers: bm rows (32, 64 or 128) and bn columns (a
+// multiple of 32 up to 256), so that few-row products, which are bound by the
+// weight stream, spread over all SMs.  (256-row tiles on pairs of CTAs, with a
+// third less L2 traffic, took the same time at every size from 512 x 4096 x
+// 4096 to 8192^3: the drain sets the pace, not the loads.)
 #pragma once
 
 #include "gemm_sm100.cuh"
@@ -59,11 +59,11 @@ struct B128GemmParams {
     int64_t sb_step;       // floats per group
     int M, N;              // rows of A; columns of C (rows of B per group)
     int num_kb;            // K / 128
-    int bm_shift;          // log2 of the tile's rows (5 .. 8)
+    int bm_shift;          // log2 of the tile's rows (5 .. 7)
     int bn;
     int m_blocks, n_blocks;
     int stages;
-    int a_bytes, b_bytes;  // per stage and CTA
+    int a_bytes, b_bytes;  // per stage
     int staging_bytes;     // kB128StagingBytes where vec_store is 0
     int epilogue;          // 0 none, 1 GELU
     int vec_store;         // 2: every row of C starts on 32 bytes, 1: on 16 bytes, 0: neither
@@ -80,8 +80,8 @@ constexpr int kB128SlotFloats = 132;   // 128 rows, 3 column blocks
 constexpr int kB128FixedBytes = 1024 + kB128ScaleSlots * kB128SlotFloats * 4 + (2 * kB128MaxStages + 8 + 2 * kB128ScaleGroups + 1) * 8 + 16;
 
 // Instruction descriptor of kind::f8f6f4: FP32 accumulator, E4M3 x E4M3, both K-major.
-MX_DEVICE_INLINE uint32_t b128_idesc(int m, int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+MX_DEVICE_INLINE uint32_t b128_idesc(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
 }
 
 // A tile's place: rows [row0, row_end) of A and C, columns n0.. of the group.
@@ -176,7 +176,7 @@ MX_DEVICE_INLINE uint32_t bf16_pair(float a, float b) {
 // VIA_TMEM: results are stored through TMEM (GELU, rows of C off 16 bytes); a
 // variant of its own, since that path in the same code costs the loop before it
 // registers (8192^3: 1200 against 1090 cycles per block).
-template <bool PAIR, int CH, bool GROUPED, bool VIA_TMEM>
+template <int CH, bool GROUPED, bool VIA_TMEM>
 __global__ void __launch_bounds__(kB128Threads, 1)
     gemm_b128_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const B128GemmParams p) {
@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(kB128Threads, 1)
     uint8_t *smem_a = smem, *smem_b = smem + S * p.a_bytes;
     float *scale_ring = reinterpret_cast<float *>(smem_b + S * p.b_bytes);   // [slots][kB128SlotFloats]
     uint8_t *staging = reinterpret_cast<uint8_t *>(scale_ring + kB128ScaleSlots * kB128SlotFloats);
-    uint64_t *full = reinterpret_cast<uint64_t *>(staging + p.staging_bytes);   // the pair leader's count both CTAs
+    uint64_t *full = reinterpret_cast<uint64_t *>(staging + p.staging_bytes);
     uint64_t *empty = full + kB128MaxStages;
     uint64_t *pfull = empty + kB128MaxStages;   // [NP]
-    uint64_t *pempty = pfull + 4;               // [NP], the leader's count both CTAs' drain warps
+    uint64_t *pempty = pfull + 4;               // [NP]
     uint64_t *sfull = pempty + 4;               // [kB128ScaleGroups]
     uint64_t *sempty = sfull + kB128ScaleGroups;
     uint64_t *mma_done = sempty + kB128ScaleGroups;
@@ -199,9 +199,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-    const int worker = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-    const int workers = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const int worker = (int)blockIdx.x, workers = (int)gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -210,7 +208,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
         }
         for (int i = 0; i < NP; ++i) {
             mbar_init(&pfull[i], 1);
-            mbar_init(&pempty[i], (PAIR ? 2 : 1) * kB128DrainWarps);
+            mbar_init(&pempty[i], kB128DrainWarps);
         }
         for (int i = 0; i < kB128ScaleGroups; ++i) {
             mbar_init(&sfull[i], 64);
@@ -223,17 +221,11 @@ __global__ void __launch_bounds__(kB128Threads, 1)
         tma_prefetch_desc(&tmB);
     }
     if (warp == 1) {
-        if (PAIR) {
-            tmem_alloc_pair(tmem_slot, 512);
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(tmem_slot, 512);
-            tmem_relinquish();
-        }
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();   // both CTAs' barriers exist before anyone signals them
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), pfull0 = smem_u32(pfull),
@@ -245,48 +237,29 @@ __global__ void __launch_bounds__(kB128Threads, 1)
         if (warp == 0 && !p.skip_producer) {
             // -------------------------------------------------------- producer
             B128Tiles<GROUPED> tiles(p, lane);
-            const uint32_t full_leader0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
             int used = 0, s = 0;
             uint32_t ph = 0;
             bool stop = false;
             B128Tile t;
             for (int i = worker; !stop && tiles.at(i, t); i += workers) {
-                const int a_row = t.row0 + (PAIR ? 128 * (int)rank : 0);
+                const int b_row = t.group * p.N + t.n0;
                 // GROUPED: of A only the 32-row boxes that hold rows of the group
-                // (each CTA's own; the leader's barrier expects both CTAs')
-                const int rows = t.row_end - t.row0;
-                const int boxes0 = GROUPED ? min(p.a_bytes / (32 * kStageKBytes), (rows + 31) / 32) : 0;
-                const int boxes1 = GROUPED && PAIR ? min(4, max(rows - 128 + 31, 0) / 32) : 0;
-                const int boxes = rank == 0 ? boxes0 : boxes1;
-                const uint32_t tx = GROUPED ? (uint32_t)((boxes0 + boxes1) * 32 * kStageKBytes + (PAIR ? 2 : 1) * p.b_bytes)
-                                            : (uint32_t)((PAIR ? 2 : 1) * (p.a_bytes + p.b_bytes));
-                const int b_row = t.group * p.N + t.n0 + (PAIR ? (p.bn / 2) * (int)rank : 0);
+                const int boxes = GROUPED ? min(p.a_bytes / (32 * kStageKBytes), (t.row_end - t.row0 + 31) / 32) : 0;
+                const uint32_t tx = (uint32_t)((GROUPED ? boxes * 32 * kStageKBytes : p.a_bytes) + p.b_bytes);
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!mbar_wait_at(empty0 + 8u * (uint32_t)s, ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
                         stop = true;
                         break;
                     }
                     if (lane == 0) {
-                        if (PAIR) {
-                            const uint32_t bar = full_leader0 + 8u * (uint32_t)s;
-                            if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
-                            if (GROUPED)
-                                for (int b = 0; b < boxes; ++b)
-                                    tma_load_2d_pair(smem_a + s * p.a_bytes + b * 32 * kStageKBytes, &tmA,
-                                                     kb * kStageKBytes, a_row + 32 * b, bar);
-                            else
-                                tma_load_2d_pair(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, a_row, bar);
-                            tma_load_2d_pair(smem_b + s * p.b_bytes, &tmB, kb * kStageKBytes, b_row, bar);
-                        } else {
-                            mbar_arrive_expect_tx(&full[s], tx);
-                            if (GROUPED)
-                                for (int b = 0; b < boxes; ++b)
-                                    tma_load_2d(smem_a + s * p.a_bytes + b * 32 * kStageKBytes, &tmA, kb * kStageKBytes,
-                                                a_row + 32 * b, &full[s]);
-                            else
-                                tma_load_2d(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, a_row, &full[s]);
-                            tma_load_2d(smem_b + s * p.b_bytes, &tmB, kb * kStageKBytes, b_row, &full[s]);
-                        }
+                        mbar_arrive_expect_tx(&full[s], tx);
+                        if (GROUPED)
+                            for (int b = 0; b < boxes; ++b)
+                                tma_load_2d(smem_a + s * p.a_bytes + b * 32 * kStageKBytes, &tmA, kb * kStageKBytes,
+                                            t.row0 + 32 * b, &full[s]);
+                        else
+                            tma_load_2d(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, t.row0, &full[s]);
+                        tma_load_2d(smem_b + s * p.b_bytes, &tmB, kb * kStageKBytes, b_row, &full[s]);
                     }
                     __syncwarp();
                     ++used;
@@ -296,16 +269,15 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     }
                 }
             }
-            // copies in flight land before this CTA (the leader, for both) may leave
-            if (rank == 0)
-                for (int u = max(0, used - S); u < used; ++u)
-                    mbar_wait_at(full0 + 8u * (uint32_t)(u % S), (uint32_t)((u / S) & 1), p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
-        } else if (warp == 1 && rank == 0) {
+            // copies in flight land before this CTA may leave
+            for (int u = max(0, used - S); u < used; ++u)
+                mbar_wait_at(full0 + 8u * (uint32_t)(u % S), (uint32_t)((u / S) & 1), p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
+        } else if (warp == 1) {
             // -------------------------------------------------------- MMA issuer
             const uint64_t desc = smem_desc(0, 16, 1024, 2);
             const uint64_t ad0 = desc | (uint64_t)((smem_u32(smem_a) >> 4) & 0x3FFFu);
             const uint64_t bd0 = desc | (uint64_t)((smem_u32(smem_b) >> 4) & 0x3FFFu);
-            const uint32_t idesc = b128_idesc(PAIR ? 256 : 128, p.bn);
+            const uint32_t idesc = b128_idesc(p.bn);
             const uint32_t leader = lane == 0 ? 1u : 0u;
             B128Tiles<GROUPED> tiles(p, lane);
             int s = 0, pi = 0;
@@ -324,17 +296,10 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     const uint64_t ad = ad0 + (uint64_t)(s * (p.a_bytes >> 4)), bd = bd0 + (uint64_t)(s * (p.b_bytes >> 4));
                     const uint32_t d = tmem + (uint32_t)(pi * kPartialCols);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (PAIR) tc_mma_pair_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, leader);
-                        else tc_mma_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, leader);
-                    }
-                    if (PAIR) {
-                        tc_commit_pair_if(&pfull[pi], 0x3, leader);
-                        tc_commit_pair_if(&empty[s], 0x3, leader);
-                    } else {
-                        tc_commit_if(&pfull[pi], leader);
-                        tc_commit_if(&empty[s], leader);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        tc_mma_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, leader);
+                    tc_commit_if(&pfull[pi], leader);
+                    tc_commit_if(&empty[s], leader);
                     if (++s == S) {
                         s = 0;
                         ph ^= 1u;
@@ -347,8 +312,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     empty_ok = mbar_test_at(pempty0 + 8u * (uint32_t)pi, pph ^ 1u);
                 }
             }
-            if (PAIR) tc_commit_pair_if(mma_done, 0x3, leader);
-            else tc_commit_if(mma_done, leader);
+            tc_commit_if(mma_done, leader);
             __syncwarp();
         } else if (warp >= 2) {
             // -------------------------------------------------------- scales
@@ -360,7 +324,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
             bool stop = false;
             B128Tile t;
             for (int i = worker; !stop && tiles.at(i, t); i += workers) {
-                const int row0 = t.row0 + (PAIR ? 128 * (int)rank : 0);
+                const int row0 = t.row0;
                 const int row_end = min(t.row_end, t.row0 + (1 << p.bm_shift));
                 const bool on0 = row0 + r0 < row_end, on1 = row0 + r0 + 64 < row_end;
                 const float *sa = p.sa + row0 + r0;
@@ -402,21 +366,19 @@ __global__ void __launch_bounds__(kB128Threads, 1)
         const int nc = min(CH, p.bn / 32 - c0);
         const uint32_t t_lane = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(32 * c0);
         uint32_t *stage = reinterpret_cast<uint32_t *>(staging) + (warp - 4) * 32 * kB128StagePitch;
-        const uint32_t pempty_leader = PAIR ? mapa_shared(pempty0, 0) : 0u;
         const uint32_t ring = smem_u32(scale_ring);
         const uint32_t lead = lane == 0 ? 1u : 0u;
         auto release = [&](uint32_t buf, uint32_t on) {   // without a branch
             tc_fence_before();
             __syncwarp();
-            if (PAIR) mbar_arrive_cluster_if(pempty_leader + 8u * buf, lead & on);
-            else mbar_arrive_at_if(pempty0 + 8u * buf, lead & on);
+            mbar_arrive_at_if(pempty0 + 8u * buf, lead & on);
         };
         B128Tiles<GROUPED> tiles(p, lane);
         uint32_t pi = 0, pph = 0, g = 0, sph = 0;
         bool stop = false, ready = false;   // ready: the next partial buffer is full, as asked ahead
         B128Tile t;
         for (int i = worker; !stop && tiles.at(i, t); i += workers) {
-            const int m0q = t.row0 + (PAIR ? 128 * (int)rank : 0) + 32 * q;
+            const int m0q = t.row0 + 32 * q;
             const int row_end = min(t.row_end, t.row0 + (1 << p.bm_shift));
             const bool any = m0q < row_end;           // warp-uniform
             // the (at most two) 128-column scale blocks under this warp's
@@ -566,13 +528,11 @@ __global__ void __launch_bounds__(kB128Threads, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        // every MMA (of the pair) has completed once mma_done has fired
+        // every MMA has completed once mma_done has fired
         mbar_wait_at(smem_u32(mma_done), 0, p.wait_limit_ns, SITE_GEMM_TAIL, nullptr);
-        if (PAIR) tmem_dealloc_pair(tmem, 512);
-        else tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, 512);
     }
     griddep_launch_dependents();
-    if (PAIR) cluster_sync();
 }
 
 }  // namespace mx

@@ -403,19 +403,15 @@ MX_DEVICE_INLINE void tc_mma_nvf4(uint32_t d, uint64_t adesc, uint64_t bdesc, ui
         : "memory");
 }
 
-// FP8 MMAs without block scales (kind::f8f6f4), issued by the threads whose
-// `issue` flag is set; the whole warp executes them with uniform operands.
-#define MX_DEFINE_F8_MMA_IF(NAME, GROUP)                                                                             \
-    MX_DEVICE_INLINE void NAME(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,     \
-                               uint32_t issue) {                                                                     \
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"                   \
-                     "@q tcgen05.mma.cta_group::" GROUP ".kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),         \
-                     "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue)                                  \
-                     : "memory");                                                                                    \
-    }
-MX_DEFINE_F8_MMA_IF(tc_mma_f8_if, "1")
-MX_DEFINE_F8_MMA_IF(tc_mma_pair_f8_if, "2")
-#undef MX_DEFINE_F8_MMA_IF
+// FP8 MMA without block scales (kind::f8f6f4), issued by the threads whose
+// `issue` flag is set; the whole warp executes it with uniform operands.
+MX_DEVICE_INLINE void tc_mma_f8_if(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate,
+                                   uint32_t issue) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue)
+                 : "memory");
+}
 
 // Register split between warpgroups: all four warps of a warpgroup execute it.
 template <int N>
@@ -495,12 +491,6 @@ MX_DEVICE_INLINE uint32_t mapa_shared(uint32_t local_saddr, uint32_t rank) {
 // about a thousand cycles per arrive here and is not needed for that order.
 MX_DEVICE_INLINE void mbar_arrive_cluster(uint32_t cluster_saddr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr) : "memory");
-}
-MX_DEVICE_INLINE void mbar_arrive_cluster_if(uint32_t cluster_saddr, uint32_t on) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                 "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_saddr),
-                 "r"(on)
-                 : "memory");
 }
 // 2D tiled TMA load into this CTA's shared memory whose completion is signalled
 // on an mbarrier of the pair's leader CTA (cta_group::2 form, no multicast).

@@ -26,50 +26,31 @@ cudaLaunchConfig_t launch_cfg(dim3 grid, int threads, size_t smem, cudaStream_t 
 }
 
 // --- tiles of the block-128 GEMM ------------------------------------------------
-struct B128Config {
-    bool pair;
-    int bm_shift;   // log2 of the tile's rows
-    int bn;
-};
-
-// The tile with the shortest run: waves of tiles times the tensor cycles of a
-// tile's K block (2 bn, whatever its rows up to 128, or 256 on a pair of CTAs)
-// plus what a block costs beside them (kBlockCycles: barriers, the drain's
-// latency).  m_blocks(rows) counts the row blocks of that height.
-template <typename MBlocks>
-B128Config b128_config(int64_t n, int sms, bool allow_pair, int max_shift, MBlocks m_blocks) {
-    constexpr double kBlockCycles = 64.0;
-    B128Config best{false, max_shift < 7 ? max_shift : 7, 256};
+// Columns of a tile: those of the shortest run, waves of tiles times the cycles
+// of a tile's K block.  The drain sets these: with two chunks per warp (up to
+// 128 columns) about 740 + 0.2 bn, with four 900 + 0.6 bn (16 x 8192 x 8192, one
+// wave either way: 64 to 128 columns 25.3 us, 160 to 224 33 to 34, 256 35.8;
+// 16 x 28672 x 8192: 128 columns in two waves 49.9 us, 224 in one 40.7).
+int b128_columns(int64_t n, int64_t row_blocks, int sms) {
+    int best = 256;
     double best_cost = 1e300;
-    for (int pair = 0; pair <= (allow_pair ? 1 : 0); ++pair) {
-        const int shift = pair ? 8 : best.bm_shift;
-        const int64_t workers = pair ? sms / 2 : sms;
-        for (int bn = 256; bn >= 32; bn -= 32) {
-            const int64_t tiles = m_blocks(1 << shift) * cdiv(n, bn);
-            const double cost = (double)cdiv(tiles, workers) * (2.0 * bn + kBlockCycles);
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = B128Config{pair != 0, shift, bn};
-            }
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        const double cost = (double)cdiv(row_blocks * cdiv(n, bn), sms) * (bn <= 128 ? 740.0 + 0.2 * bn : 900.0 + 0.6 * bn);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = bn;
         }
     }
     return best;
 }
 
-template <bool PAIR, int CH, bool GROUPED, bool VIA>
+template <int CH, bool GROUPED, bool VIA>
 mx_status launch_b128_t(const CUtensorMap &ta, const CUtensorMap &tb, const B128GemmParams &p, int workers, size_t smem,
                         cudaStream_t st) {
-    const auto kern = gemm_b128_kernel<PAIR, CH, GROUPED, VIA>;
+    const auto kern = gemm_b128_kernel<CH, GROUPED, VIA>;
     if (smem_limit_once(reinterpret_cast<const void *>(kern), kSmemLimit) != cudaSuccess) return MX_ERR_CUDA;
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(PAIR ? 2 * workers : workers), 1, 1), kB128Threads, smem, st, attr);
-    if (PAIR) {
-        cudaLaunchAttribute &c = attr[cfg.numAttrs++];
-        c.id = cudaLaunchAttributeClusterDimension;
-        c.val.clusterDim.x = 2;
-        c.val.clusterDim.y = 1;
-        c.val.clusterDim.z = 1;
-    }
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)workers, 1, 1), kB128Threads, smem, st, attr);
     cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
     return last_launch();
 }
@@ -81,24 +62,16 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     const int64_t G = groups ? groups->count : 1;
     const int sms = num_sms();
     const int cap = g_max_gemm_ctas.load();
-    B128Config cfg;
-    if (groups) {
-        // sizes of the groups are device data: their mean decides
-        const int64_t mean = cdiv(M, G);
-        const int shift = mean <= 24 ? 5 : (mean <= 48 ? 6 : 7);
-        cfg = b128_config(N, sms, mean > 192 && N > 128 && g_pair_enabled.load(), shift, [&](int64_t bm) {
-            return (G < M ? G : M) / 2 + cdiv(M, bm);   // half a block of each group is ragged
-        });
-    } else {
-        const int shift = M <= 32 ? 5 : (M <= 64 ? 6 : 7);
-        cfg = b128_config(N, sms, M > 128 && N > 128 && g_pair_enabled.load(), shift,
-                          [&](int64_t bm) { return cdiv(M, bm); });
-    }
     B128GemmParams p{};
-    const int a_rows = cfg.pair ? 128 : 1 << cfg.bm_shift;
-    const int b_rows = cfg.pair ? cfg.bn / 2 : cfg.bn;
-    p.a_bytes = a_rows * kStageKBytes;
-    p.b_bytes = b_rows * kStageKBytes;
+    // Rows of a tile: the matrix's up to 128; 128 for groups, whose sizes the
+    // host does not know (a tile brings only the boxes of A that it needs: 64
+    // experts of 8 rows 93.1 / 89.1 / 90.0 us with 32 / 64 / 128 rows, of 32 rows
+    // 115.6 / 96.6 / 93.9, 32 experts of 64 rows 174 / 106 / 99.7).
+    p.bm_shift = groups || M > 64 ? 7 : (M > 32 ? 6 : 5);
+    p.m_blocks = (int)cdiv(M, (int64_t)1 << p.bm_shift);
+    p.bn = b128_columns(N, groups ? (G < M ? G : M) + M / 256 : p.m_blocks, sms);
+    p.a_bytes = (1 << p.bm_shift) * kStageKBytes;
+    p.b_bytes = p.bn * kStageKBytes;
     const auto base = reinterpret_cast<uintptr_t>(C);
     p.vec_store = ldc % 16 == 0 && base % 32 == 0 ? 2 : (ldc % 8 == 0 && base % 16 == 0 ? 1 : 0);
     p.staging_bytes = p.vec_store ? 0 : kB128StagingBytes;
@@ -107,8 +80,8 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     if (p.stages > kB128MaxStages) p.stages = kB128MaxStages;
     const size_t smem = (size_t)fixed + (size_t)p.stages * (p.a_bytes + p.b_bytes);
     CUtensorMap ta, tb;
-    if (!make_tmap_u8(&ta, A->codes, M, K, groups ? 32 : a_rows)) return MX_ERR_CUDA;
-    if (!make_tmap_u8(&tb, B->codes, G * N, K, b_rows)) return MX_ERR_CUDA;
+    if (!make_tmap_u8(&ta, A->codes, M, K, groups ? 32 : 1 << p.bm_shift)) return MX_ERR_CUDA;
+    if (!make_tmap_u8(&tb, B->codes, G * N, K, p.bn)) return MX_ERR_CUDA;
     p.sa = reinterpret_cast<const float *>(A->scales);
     p.sb = reinterpret_cast<const float *>(B->scales);
     p.C = C;
@@ -118,33 +91,24 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     p.M = (int)M;
     p.N = (int)N;
     p.num_kb = (int)(K / 128);
-    p.bm_shift = cfg.bm_shift;
-    p.bn = cfg.bn;
-    p.m_blocks = (int)cdiv(M, (int64_t)1 << cfg.bm_shift);
-    p.n_blocks = (int)cdiv(N, cfg.bn);
+    p.n_blocks = (int)cdiv(N, p.bn);
     p.epilogue = epilogue;
     p.skip_producer = g_skip_producer.load();
     p.wait_limit_ns = g_wait_limit_ns.load();
     if (groups) p.groups = Groups{groups->offsets, groups->count, (int)M};
     // an upper bound of the tiles: a ragged block per group
-    const int64_t blocks = groups ? (M < (M >> cfg.bm_shift) + G ? M : (M >> cfg.bm_shift) + G) : p.m_blocks;
-    const int64_t tiles = blocks * p.n_blocks;
+    const int64_t tiles = (groups ? group_bands(M, G) : p.m_blocks) * p.n_blocks;
     if (tiles > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
-    int64_t workers = cfg.pair ? sms / 2 : sms;
-    if (cap > 0 && cap < sms) workers = cfg.pair ? (cap + 1) / 2 : cap;
-    if (workers > tiles) workers = tiles;
-    const bool via = epilogue == MX_EPI_GELU || p.vec_store == 0, wide = cfg.bn > 128;
-#define MX_LAUNCH(PAIR, CH)                                                                            \
-    return groups ? (via ? launch_b128_t<PAIR, CH, true, true>(ta, tb, p, (int)workers, smem, st)      \
-                         : launch_b128_t<PAIR, CH, true, false>(ta, tb, p, (int)workers, smem, st))    \
-                  : (via ? launch_b128_t<PAIR, CH, false, true>(ta, tb, p, (int)workers, smem, st)     \
-                         : launch_b128_t<PAIR, CH, false, false>(ta, tb, p, (int)workers, smem, st))
-    if (cfg.pair) {
-        if (wide) MX_LAUNCH(true, 4);
-        MX_LAUNCH(true, 2);
-    }
-    if (wide) MX_LAUNCH(false, 4);
-    MX_LAUNCH(false, 2);
+    int workers = cap > 0 && cap < sms ? cap : sms;
+    if (workers > tiles) workers = (int)tiles;
+    const bool via = epilogue == MX_EPI_GELU || p.vec_store == 0;
+#define MX_LAUNCH(CH)                                                                     \
+    return groups ? (via ? launch_b128_t<CH, true, true>(ta, tb, p, workers, smem, st)    \
+                         : launch_b128_t<CH, true, false>(ta, tb, p, workers, smem, st))  \
+                  : (via ? launch_b128_t<CH, false, true>(ta, tb, p, workers, smem, st)   \
+                         : launch_b128_t<CH, false, false>(ta, tb, p, workers, smem, st))
+    if (p.bn > 128) MX_LAUNCH(4);
+    MX_LAUNCH(2);
 #undef MX_LAUNCH
 }
 
@@ -332,8 +296,6 @@ mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, i
     if (p.slab > 4) p.slab = 4;
     if (p.slab < 1) p.slab = 1;
     p.slabs = (int)cdiv(tiles, p.slab);
-    // a gathered source that does not stay in L2 beside the output
-    p.interleave = row_index != nullptr && src_rows * K * 2 > (int64_t)32 << 20 ? 1 : 0;
     switch (fmt) {
     case MX_FP8_B128: launch_quantize_grouped<FMT_B128>(p, bands, st); break;
     case MX_MXFP8_E4M3: launch_quantize_grouped<FMT_E4M3>(p, bands, st); break;

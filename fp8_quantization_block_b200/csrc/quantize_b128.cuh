@@ -186,13 +186,6 @@ __global__ void __launch_bounds__(256) dequantize_b128_kernel(const uint8_t *__r
 // scales.  A CTA takes one band (its group found by a warp) and p.slab K tiles
 // of 128 columns, the next tile's loads in flight while one is quantized, with
 // the arithmetic of the plain kernels.
-//
-// Order of the bands.  A gather of k choices per token reads every row k
-// times, and a source larger than L2 would come from HBM each time.  Within an
-// expert the rows are in the tokens' order, so bands at the same relative
-// place of their experts read neighbouring tokens: with `interleave` the CTAs
-// run through all experts side by side, in order of (band / bands of its
-// expert), and the rows' later reads are served by L2.
 struct GroupedQuantParams {
     const uint16_t *src;
     int64_t ld;
@@ -205,76 +198,9 @@ struct GroupedQuantParams {
     int64_t sf_tiles_k;
     int64_t pitch;               // FP8_B128: floats per K block
     int slab, slabs;             // K tiles per CTA, CTAs per band
-    int interleave;
     const float *gscale;         // NVFP4: g
     float *gscale_out;           // NVFP4, nullable: receives g
 };
-
-// The band that CTA `i` of the interleaved order works on (warp-collective;
-// nb: shared memory for MAX groups).  With C(x) = sum over the groups of
-// floor(bands x / kSteps), the number of bands at relative places below x /
-// kSteps, the i-th band lies in the step with C(x - 1) <= i < C(x), found by
-// bisection, and is the (i - C(x - 1))-th of that step's bands in group order.
-// Each lane holds a run of consecutive groups.
-constexpr int kMaxGroups = 1024;
-struct Band {
-    int band, row0, row1;   // band of the scale buffer; rows
-};
-MX_DEVICE_INLINE Band interleaved_band(const Groups &g, int i, int *nb, int lane) {
-    constexpr int kSteps = 1024;
-    const int per = (g.count + 31) / 32, e0 = lane * per, e1 = min(e0 + per, g.count);
-    int mine = 0;
-    for (int e = e0; e < e1; ++e) {
-        const int s = min(max(g.offsets[e], 0), g.rows), t = min(max(g.offsets[e + 1], 0), g.rows);
-        nb[e] = (max(t - s, 0) + 127) >> 7;
-        mine += nb[e];
-    }
-    __syncwarp();
-    const int total = (int)__reduce_add_sync(0xffffffffu, (unsigned)mine);
-    if (i >= total) return Band{i, 0, 0};
-    auto below = [&](int x) {   // this lane's part of C(x)
-        int c = 0;
-        for (int e = e0; e < e1; ++e) c += (int)((uint64_t)(uint32_t)nb[e] * (uint32_t)x / kSteps);
-        return c;
-    };
-    int lo = 0, hi = kSteps;   // C(lo) <= i < C(hi)
-    while (hi - lo > 1) {
-        const int x = (lo + hi) / 2;
-        if ((int)__reduce_add_sync(0xffffffffu, (unsigned)below(x)) <= i) lo = x;
-        else hi = x;
-    }
-    const int b0 = below(lo), d = below(hi) - b0;
-    int incl = d, bands = mine;   // inclusive prefixes over the lanes
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, bands, o);
-        if (lane >= o) {
-            incl += u;
-            bands += v;
-        }
-    }
-    int k = i - (int)__reduce_add_sync(0xffffffffu, (unsigned)b0);
-    const int l = __ffs(__ballot_sync(0xffffffffu, incl > k)) - 1;
-    int band = 0, row0 = 0, row1 = 0;
-    if (lane == l) {
-        k -= incl - d;
-        band = bands - mine;
-        for (int e = e0; e < e1; ++e) {
-            const int a = (int)((uint64_t)(uint32_t)nb[e] * (uint32_t)lo / kSteps);
-            const int n = (int)((uint64_t)(uint32_t)nb[e] * (uint32_t)hi / kSteps) - a;
-            if (k < n) {
-                const int s = min(max(g.offsets[e], 0), g.rows), t = min(max(g.offsets[e + 1], 0), g.rows);
-                band += a + k;
-                row0 = s + (a + k) * 128;
-                row1 = min(t, row0 + 128);
-                break;
-            }
-            k -= n;
-            band += nb[e];
-        }
-    }
-    return Band{__shfl_sync(0xffffffffu, band, l), __shfl_sync(0xffffffffu, row0, l), __shfl_sync(0xffffffffu, row1, l)};
-}
 
 // Codes of 16 values (v0, v1) of row `row`, columns col .. col + 15, stored where
 // `ok`, and their block's scale byte, returned: the arithmetic of
@@ -320,8 +246,7 @@ template <int FMT>
 __global__ void __launch_bounds__(kQThreads, 4) quantize_grouped_kernel(GroupedQuantParams p) {
     constexpr int kPasses = kQTileRows / 32;
     __shared__ NvTables nvt;
-    __shared__ int nb[kMaxGroups];
-    __shared__ Band info;
+    __shared__ int rows_of[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l8 = lane & 7;
     const int bi = (int)(blockIdx.x / (unsigned)p.slabs);
     const int tile0 = (int)(blockIdx.x - (unsigned)bi * (unsigned)p.slabs) * p.slab;
@@ -329,18 +254,17 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_grouped_kernel(GroupedQ
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 0) {
-        Band b{bi, 0, 0};
-        if (p.interleave) {
-            b = interleaved_band(p.groups, bi, nb, lane);
-        } else {
-            GroupWalk walk(p.groups, 7, lane);
-            GroupBlock g;
-            if (walk.find(bi, g)) {
-                b.row0 = g.start + (bi - g.first) * kQTileRows;
-                b.row1 = min(g.end, b.row0 + kQTileRows);
-            }
+        int r0 = 0, r1 = 0;
+        GroupWalk walk(p.groups, 7, lane);
+        GroupBlock g;
+        if (walk.find(bi, g)) {
+            r0 = g.start + (bi - g.first) * kQTileRows;
+            r1 = min(g.end, r0 + kQTileRows);
         }
-        if (lane == 0) info = b;
+        if (lane == 0) {
+            rows_of[0] = r0;
+            rows_of[1] = r1;
+        }
     }
     NvScale ns{1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
     if (FMT == FMT_NVFP4) {
@@ -352,7 +276,7 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_grouped_kernel(GroupedQ
     __syncthreads();
     // from here on every warp runs by itself: its rows are 32 i + 4 warp .. + 3
     // of the band, and its scale bytes go straight to their places
-    const int64_t band = info.band, row0 = info.row0, row1 = info.row1;
+    const int64_t band = bi, row0 = rows_of[0], row1 = rows_of[1];
     const int passes = (int)(row1 - row0 + 31) / 32;   // passes that hold rows
     if (FMT == FMT_B128 && passes == 0) return;
     int from[kPasses];   // this thread's source rows, -1 for none
