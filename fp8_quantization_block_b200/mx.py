@@ -258,12 +258,17 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _elsewhere(t: torch.Tensor) -> bool:
-    """Is the tensor on another device than the current one?"""
+def _elsewhere(t: torch.Tensor, stream=None):
+    """The context a call on t has to run in, or None: t's device where it is not the current one, and a stream that
+    the caller names, so that what the call allocates belongs to that stream too."""
     at = t.get_device()
     if at < 0:
         raise ValueError("CUDA tensors are wanted")
-    return at != torch._C._cuda_getDevice()
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError("a stream of the tensors' device is wanted")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(at) if at != torch._C._cuda_getDevice() else None
 
 
 def _ptr(t: torch.Tensor | None):
@@ -298,8 +303,8 @@ def empty(fmt: int, rows: int, cols: int, device="cuda") -> MxTensor:
 def quantize(x: torch.Tensor, fmt: int, gscale: torch.Tensor | None = None, out: MxTensor | None = None,
              stream=None) -> MxTensor:
     """bf16 [M, K] CUDA tensor (row pitch x.stride(0)) -> MxTensor."""
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
+    if (ctx := _elsewhere(x)) is not None:
+        with ctx:
             return quantize(x, fmt, gscale, out, stream)
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     M, K = x.shape
@@ -347,8 +352,8 @@ def qsnr_sums(t: MxTensor, x: torch.Tensor, out: torch.Tensor | None = None, str
 
 
 def dequantize(t: MxTensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    if _elsewhere(t.codes):
-        with torch.cuda.device(t.codes.device):
+    if (ctx := _elsewhere(t.codes)) is not None:
+        with ctx:
             return dequantize(t, out, stream)
     out = out if out is not None else torch.empty((t.rows, t.cols), dtype=torch.bfloat16, device=t.codes.device)
     check(mx_dequantize(t.c(), out.data_ptr(), out.stride(0), _stream(stream)), "mx_dequantize")
@@ -356,22 +361,31 @@ def dequantize(t: MxTensor, out: torch.Tensor | None = None, stream=None) -> tor
 
 
 def gemm(A: MxTensor, B: MxTensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    if _elsewhere(A.codes):
-        with torch.cuda.device(A.codes.device):
+    if (ctx := _elsewhere(A.codes)) is not None:
+        with ctx:
             return gemm(A, B, out, stream)
     out = out if out is not None else torch.empty((A.rows, B.rows), dtype=torch.bfloat16, device=A.codes.device)
     check(mx_gemm(A.c(), B.c(), out.data_ptr(), out.stride(0), _stream(stream)), "mx_gemm")
     return out
 
 
+def _act_fmt(W: MxTensor) -> int:
+    """The format of the activations that go with W."""
+    return MX_FP8_B128 if W.fmt == MX_FP8_B128X128 else W.fmt
+
+
 def gemm_fused_act(x: torch.Tensor, W: MxTensor, out: torch.Tensor | None = None, epilogue: int = MX_EPI_NONE,
                    amax_out: torch.Tensor | None = None, x_gscale: torch.Tensor | None = None,
                    x_amax: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                    stream=None, x_fmt: int | None = None) -> torch.Tensor:
-    """x_fmt: the format X is quantized to (default W's; any MX format pairs with an MX W)."""
+    """x_fmt: the format X is quantized to (default W's, FP8_B128 where that is FP8_B128X128; any MX format pairs with
+    an MX W)."""
+    if (ctx := _elsewhere(x)) is not None:
+        with ctx:
+            return gemm_fused_act(x, W, out, epilogue, amax_out, x_gscale, x_amax, workspace, stream, x_fmt)
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     M, K = x.shape
-    fmt = W.fmt if x_fmt is None else x_fmt
+    fmt = _act_fmt(W) if x_fmt is None else x_fmt
     out = out if out is not None else torch.empty((M, W.rows), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = fused_workspace(fmt, M, K, x.device)
@@ -390,6 +404,8 @@ def fused_workspace(fmt: int, M: int, K: int, device="cuda", split: bool = True)
 
 
 # ----------------------------------------------------------------- mixture of experts
+# A stream that the caller names is the current one for the whole call: what the call allocates, results included,
+# belongs to it, as under `with torch.cuda.stream(...)`.
 @dataclass
 class Routing:
     """What mx_route writes: groups of slots, and slots from and to the tokens' choices."""
@@ -430,9 +446,9 @@ def route(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = None
     """Expert ids [tokens, choices] (int32 or int64; others than 0 .. experts - 1 have no slot) -> Routing."""
     _need(ids.dtype in (torch.int32, torch.int64) and ids.dim() == 2 and ids.is_contiguous(),
           "ids: a contiguous int32 or int64 matrix is wanted")
-    if _elsewhere(ids):
-        with torch.cuda.device(ids.device):
-            return route(ids, experts, workspace, stream)
+    if (ctx := _elsewhere(ids, stream)) is not None:
+        with ctx:
+            return route(ids, experts, workspace)
     tokens, choices = ids.shape
     n, dev = tokens * choices, ids.device
     _need(choices >= 1 and 1 <= experts <= MX_MAX_GROUPS, "at least one choice and 1 to MX_MAX_GROUPS experts are wanted")
@@ -466,9 +482,9 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, row_index
     """Rows of x (x[row_index[t]], or x itself) quantized for gemm_grouped.  NVFP4 wants gscale (g)."""
     _rows_ok(x, "x")
     groups = _groups(offsets)
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
-            return quantize_grouped(x, offsets, fmt, row_index, gscale, out, stream)
+    if (ctx := _elsewhere(x, stream)) is not None:
+        with ctx:
+            return quantize_grouped(x, offsets, fmt, row_index, gscale, out)
     K = x.shape[1]
     if row_index is not None:
         _need(row_index.dtype == torch.int32 and row_index.dim() == 1 and row_index.is_contiguous(),
@@ -489,9 +505,9 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, row_index
 def quantize_experts(w: torch.Tensor, fmt: int, stream=None) -> MxTensor:
     """bf16 [experts, N, K] -> the experts' matrices one after another, as gemm_grouped takes them for B (rows N)."""
     _need(w.dtype == torch.bfloat16 and w.dim() == 3 and w.stride(2) == 1, "w: bf16 [experts, N, K] is wanted")
-    if _elsewhere(w):
-        with torch.cuda.device(w.device):
-            return quantize_experts(w, fmt, stream)
+    if (ctx := _elsewhere(w, stream)) is not None:
+        with ctx:
+            return quantize_experts(w, fmt)
     E, N, K = w.shape
     cb, sb = mx_codes_bytes(fmt, N, K), mx_scales_bytes(fmt, N, K)
     codes = torch.empty(max(E * cb, 1), dtype=torch.uint8, device=w.device)
@@ -510,9 +526,9 @@ def gemm_grouped(A: MxTensor, B: MxTensor, offsets: torch.Tensor, out: torch.Ten
     """C[t] = f(A[t] B_g^T) for the rows t of every group g; B as quantize_experts gives it.  bf16 [A.rows, B.rows],
     rows of no group left as they are."""
     groups = _groups(offsets)
-    if _elsewhere(A.codes):
-        with torch.cuda.device(A.codes.device):
-            return gemm_grouped(A, B, offsets, out, epilogue, stream)
+    if (ctx := _elsewhere(A.codes, stream)) is not None:
+        with ctx:
+            return gemm_grouped(A, B, offsets, out, epilogue)
     E = groups.count
     _need(_nbytes(A.codes) >= mx_codes_bytes(A.fmt, A.rows, A.cols) and
           _nbytes(A.scales) >= mx_grouped_scales_bytes(A.fmt, A.rows, E, A.cols), "A: a buffer is too small")
@@ -537,9 +553,9 @@ def combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, out: tor
     _need(slot.dtype == torch.int32 and slot.dim() == 2 and slot.is_contiguous(), "slot: a contiguous int32 matrix is wanted")
     _need(weights.dtype == torch.float32 and weights.shape == slot.shape and weights.is_contiguous(),
           "weights: a contiguous float32 matrix of slot's shape is wanted")
-    if _elsewhere(y):
-        with torch.cuda.device(y.device):
-            return combine(y, slot, weights, out, stream)
+    if (ctx := _elsewhere(y, stream)) is not None:
+        with ctx:
+            return combine(y, slot, weights, out)
     tokens, choices = slot.shape
     rows, cols = y.shape
     if out is None:
@@ -560,13 +576,18 @@ def experts_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W1: M
 
     W1 [experts x N x K] and W2 [experts x K' x N] as quantize_experts gives them; activations are quantized to
     act_fmt (default: the format that goes with the weights').  NVFP4 wants the activations' g (x_gscale, h_gscale)."""
-    fmt = act_fmt if act_fmt is not None else (MX_FP8_B128 if W1.fmt == MX_FP8_B128X128 else W1.fmt)
+    if (ctx := _elsewhere(x, stream)) is not None:
+        with ctx:
+            return experts_mlp(x, ids, weights, W1, W2, x_gscale, h_gscale, act_fmt)
+    fmt = _act_fmt(W1) if act_fmt is None else act_fmt
     experts = W1.codes.numel() // max(mx_codes_bytes(W1.fmt, W1.rows, W1.cols), 1)
-    r = route(ids, experts, stream=stream)
-    h = gemm_grouped(quantize_grouped(x, r.offsets, fmt, row_index=r.row_token, gscale=x_gscale, stream=stream), W1,
-                     r.offsets, epilogue=MX_EPI_GELU, stream=stream)
-    y = gemm_grouped(quantize_grouped(h, r.offsets, fmt, gscale=h_gscale, stream=stream), W2, r.offsets, stream=stream)
-    return combine(y, r.slot, weights, stream=stream)
+    _need(x.shape[0] == ids.shape[0], "x and ids: one row per token")
+    _need(weights.shape == ids.shape, "weights: one per choice")
+    r = route(ids, experts)
+    h = gemm_grouped(quantize_grouped(x, r.offsets, fmt, row_index=r.row_token, gscale=x_gscale), W1, r.offsets,
+                     epilogue=MX_EPI_GELU)
+    y = gemm_grouped(quantize_grouped(h, r.offsets, fmt, gscale=h_gscale), W2, r.offsets)
+    return combine(y, r.slot, weights)
 
 
 def check_device_error(stream=None) -> None:

@@ -214,7 +214,8 @@ mx_status mx_qsnr(const mx_tensor *q, const void *src_bf16, int64_t ld_src, doub
  * FP6 or FP4 operand 32-byte aligned (else MX_ERR_MISALIGNED).  NVFP4 pairs
  * only with NVFP4, and FP8_B128 (A) only with FP8_B128X128 (B): there the
  * tensor core sums each block's products in FP32, and the CUDA cores add them
- * up times the two scales, in FP32.  C is bf16 [M x N] with row pitch ldc
+ * up times the two scales, in FP32 (the scales' product first: outside FP32's
+ * normal range it overflows or loses bits).  C is bf16 [M x N] with row pitch ldc
  * (ldc >= N).  Accuracy contract:
  *   |C - C_ref| <= 2^-8 |C_ref| + 1e-4 (|A_dq| |B_dq|^T)  elementwise.       */
 mx_status mx_gemm(const mx_tensor *A, const mx_tensor *B, void *C_bf16, int64_t ldc, void *stream);

@@ -36,19 +36,15 @@ def test_many_rows(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(300, 700, 256), (40, 700, 256)])
-def test_single_cta_and_several_tiles_per_cta(M, N, K):
-    """The same bits from CTA pairs or single CTAs on one tile or many per CTA is not promised (tile shapes differ),
-    the contract is; the grid cap makes every CTA walk several tiles."""
+def test_several_tiles_per_cta(M, N, K):
+    """The grid cap makes every CTA walk several tiles; the grid does not change how a tile is summed."""
     try:
         mx.check(mx.mx_debug_set(mx.MX_DEBUG_MAX_GEMM_CTAS, 2))
         _, _, c2 = run(M, N, K)
-        mx.check(mx.mx_debug_set(mx.MX_DEBUG_PAIR_GEMM, 0))
-        run(M, N, K)
     finally:
         mx.mx_debug_set(mx.MX_DEBUG_MAX_GEMM_CTAS, 0)
-        mx.mx_debug_set(mx.MX_DEBUG_PAIR_GEMM, 1)
     _, _, c = run(M, N, K)
-    assert torch.equal(c, c2)     # the grid does not change how a tile is summed
+    assert torch.equal(c, c2)
 
 
 def test_row_pitch_leaves_the_rest():
@@ -117,3 +113,41 @@ def test_same_bits_from_call_to_call_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, c)
+
+
+def test_two_streams_at_once():
+    """Calls of two streams that overlap on the GPU do not touch one another."""
+    a, b, c = run(200, 2048, 1024)
+    a2, b2, c2 = run(16, 4096, 2048)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    o1, o2 = [torch.empty_like(c) for _ in range(8)], [torch.empty_like(c2) for _ in range(8)]
+    for i in range(8):
+        mx.gemm(a, b, out=o1[i], stream=s1)
+        mx.gemm(a2, b2, out=o2[i], stream=s2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, c) for o in o1) and all(torch.equal(o, c2) for o in o2)
+    mx.check_device_error()
+
+
+def test_fused_call_without_allocation_in_a_graph():
+    """The fused call's quantized operand lives in the caller's workspace, through a capture and its replays."""
+    M, N, K = 150, 400, 640
+    x = activations(8, M, K)
+    w = mx.quantize(weights(9, N, K), mx.MX_FP8_B128X128)
+    ws = mx.fused_workspace(mx.MX_FP8_B128, M, K)
+    want = mx.gemm(mx.quantize(x, mx.MX_FP8_B128), w)
+    out = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        mx.gemm_fused_act(x, w, out=out, workspace=ws)      # x_fmt: the one that goes with w
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mx.gemm_fused_act(x, w, x_fmt=mx.MX_FP8_B128, out=out, workspace=ws)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

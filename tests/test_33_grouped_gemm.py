@@ -128,7 +128,7 @@ def test_several_tiles_per_cta(fa, fb, gelu):
             assert gemm_error(c[i:j], v[i:j], expert_values(w, g), gelu) <= 1.0
 
 
-def test_large_groups_on_cta_pairs():
+def test_groups_of_several_blocks():
     counts, N, K = [600, 1, 333, 256], 520, 384
     x, o, od, a = quantized(counts, 6, K)
     w = mx.quantize_experts(weights(24, 4, N, K), 8)
@@ -186,3 +186,69 @@ def test_helpers_read_the_layouts():
         t = mx.quantize(x, fmt)
         s = scale_values(sf_at(t.scales, torch.arange(70, device="cuda"), 8), fmt).repeat_interleave(32, 1)
         assert torch.equal((element_values(t.codes, fmt, 70, 256) * s).bfloat16(), mx.dequantize(t))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(seed):
+    """Groups, widths and depths at random, empty groups and groups of one row among them."""
+    g = torch.Generator().manual_seed(seed)
+
+    def r(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=g))
+    fa, fb = PAIRS[seed % len(PAIRS)]
+    E, N, K = r(1, 40) if seed % 6 else 300, r(1, 700), 128 * r(1, 9)
+    counts = [r(0, 90) * (r(0, 3) > 0) * (1 if r(0, 9) else 6) for _ in range(E)]
+    x, o, od, a = quantized(counts, fa, K, behind=r(0, 5), seed=seed)
+    w = mx.quantize_experts(weights(seed, E, N, K), fb)
+    gelu = seed % 3 == 0
+    c = torch.full((a.rows, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.gemm_grouped(a, w, od, out=c, epilogue=mx.MX_EPI_GELU if gelu else mx.MX_EPI_NONE)
+    torch.cuda.synchronize()
+    mx.check_device_error()
+    v = grouped_values(a, o)
+    for e, (i, j) in enumerate(zip(o, o[1:])):
+        if j > i:
+            assert gemm_error(c[i:j], v[i:j], expert_values(w, e), gelu) <= 1.0, (E, N, K, e)
+    assert (c[o[-1]:] == 9).all()
+
+
+@pytest.mark.parametrize("fa,fb", [B, (0, 0)])
+def test_a_nan_stays_in_its_row_and_column(fa, fb):
+    """NaN codes in the rows behind the last group, in another group and in one weight row touch nothing else."""
+    counts, N, K = [20, 30], 300, 256
+    x, o, od, a = quantized(counts, fa, K, behind=14)
+    w = mx.quantize_experts(weights(41, 2, N, K), fb)
+    want = mx.gemm_grouped(a, w, od)[:50].clone()
+    codes = a.codes.view(-1, K)
+    codes[50:] = 0x7F
+    codes[25] = 0x7F
+    w.codes.view(2, N, K)[1, 7] = 0x7F
+    c = mx.gemm_grouped(a, w, od)[:50]
+    assert c[25].isnan().all() and c[20:, 7].isnan().all()
+    keep = torch.ones(50, N, dtype=torch.bool, device="cuda")
+    keep[25] = False
+    keep[20:, 7] = False
+    assert torch.equal(c[keep], want[keep])
+
+
+@pytest.mark.parametrize("fa,fb", [(6, 8), (0, 0), (3, 3), (1, 2)])
+def test_a_stalled_producer_is_reported(fa, fb):
+    """The producer issues nothing: the bounded waits run out, the call ends and is reported, and the next is right."""
+    counts, N, K = [40, 0, 9], 300, 2560
+    x, o, od, a = quantized(counts, fa, K)
+    w = mx.quantize_experts(weights(51, 3, N, K), fb)
+    c = mx.gemm_grouped(a, w, od)
+    torch.cuda.synchronize()
+    assert mx.mx_check_device_error()[0] == mx.MX_OK
+    try:
+        mx.check(mx.mx_debug_set(mx.MX_DEBUG_WAIT_LIMIT_NS, 50_000_000))
+        mx.check(mx.mx_debug_set(mx.MX_DEBUG_SKIP_PRODUCER, 1))
+        mx.gemm_grouped(a, w, od)
+        status, info = mx.mx_check_device_error()
+    finally:
+        mx.mx_debug_set(mx.MX_DEBUG_SKIP_PRODUCER, 0)
+        mx.mx_debug_set(mx.MX_DEBUG_WAIT_LIMIT_NS, 1_000_000_000)
+    assert status == mx.MX_ERR_TIMEOUT and info[0] & 1 and info[3] >= 1
+    assert mx.mx_check_device_error()[0] == mx.MX_OK
+    assert torch.equal(mx.gemm_grouped(a, w, od), c)
+    assert mx.mx_check_device_error()[0] == mx.MX_OK

@@ -150,3 +150,62 @@ def test_experts_mlp_in_a_graph_and_on_a_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want2)
+
+
+def test_a_named_stream_owns_what_the_call_allocates():
+    """The call's own tensors belong to the named stream: what is allocated and written right after it on the current
+    stream does not touch them."""
+    x, ids, p, W1, W2 = experts_case(6, 8, tokens=2000, choices=4, N=1024)
+    want = mx.experts_mlp(x, ids, p, W1, W2)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        got = mx.experts_mlp(x, ids, p, W1, W2, stream=s)
+        junk = [torch.full((1 << 20,), 0xAB, dtype=torch.uint8, device="cuda") for _ in range(40)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del junk
+    ids2 = torch.randint(0, 9, (3000, 8), device="cuda")
+    a, b = mx.route(ids2, 9), mx.route(ids2, 9, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a.slot, b.slot) and torch.equal(a.row_token, b.row_token)
+
+
+@pytest.mark.parametrize("n,experts", [(600_000, 40), (300_000, 1024), (262_145, 2)])
+def test_route_of_many_choices(n, experts):
+    """Over 128 chunks' worth: larger chunks."""
+    ids = torch.randint(-1, experts + 1, (n, 1), generator=torch.Generator().manual_seed(n)).int()
+    r = mx.route(ids.cuda(), experts)
+    flat = ids.view(-1)
+    ok = (flat >= 0) & (flat < experts)
+    order = torch.argsort(torch.where(ok, flat, experts), stable=True)[:int(ok.sum())]
+    slot = torch.full((n,), -1, dtype=torch.int32)
+    slot[order] = torch.arange(order.numel(), dtype=torch.int32)
+    assert torch.equal(r.slot.view(-1).cpu(), slot)
+    assert torch.equal(r.row_token[:order.numel()].cpu(), order.int()) and (r.row_token[order.numel():] == -1).all()
+    assert torch.equal(r.offsets.cpu(), torch.nn.functional.pad(
+        torch.bincount(flat[ok], minlength=experts).cumsum(0), (1, 0)).int())
+
+
+def test_offsets_past_32_bits():
+    """Rows whose element offset needs 64 bits: the gather's source, combine's rows, the product's output."""
+    rows, cols = 540_000, 4096                       # 2.2 G elements
+    y = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    tail = activations(3, 40, cols)
+    y[-40:] = tail
+    slot = torch.arange(rows - 40, rows, dtype=torch.int32, device="cuda").view(20, 2)
+    w = torch.rand(20, 2, generator=torch.Generator().manual_seed(1)).cuda()
+    near = torch.arange(40, dtype=torch.int32, device="cuda").view(20, 2)
+    assert torch.equal(mx.combine(y, slot, w), mx.combine(tail, near, w))
+    off = torch.tensor([0, 25, 40], dtype=torch.int32, device="cuda")
+    for fmt in (6, 0):
+        a = mx.quantize_grouped(y, off, fmt, row_index=slot.view(-1))
+        b = mx.quantize_grouped(tail, off, fmt, row_index=near.view(-1))
+        assert torch.equal(a.codes, b.codes)
+    del y
+    M, N = 34_000, 65_536                            # 2.2 G elements of output
+    a = mx.quantize(activations(4, M, 128), 6)
+    b = mx.quantize(weights(5, N, 128), 8)
+    c = mx.gemm(a, b)
+    last = mx.MxTensor(6, 100, 128, a.codes[(M - 100) * 128:], a.scales.view(torch.float32)[M - 100:M].contiguous(), None)
+    assert torch.equal(c[-100:], mx.gemm(last, b))
