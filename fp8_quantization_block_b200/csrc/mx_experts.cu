@@ -173,8 +173,39 @@ mx_status check_groups(const mx_groups *g) {
     return MX_OK;
 }
 
+// By source row (quantize_scatter_kernel) rather than by destination: where the
+// rows that the gather would read again are worth two more launches.  us by
+// destination / by source, FP8_B128: 32 x 8 places of 4096 columns 5.2 / 6.1,
+// 64 x 8 6.1 / 6.3, 4096 x 4 of 512 8.4 / 7.2, 1024 x 2 of 4096 8.5 / 6.7,
+// 256 x 8 12.8 / 7.4, 1024 x 8 24.4 / 12.1, 16384 x 4 130 / 79.  A warp takes
+// 512 columns at once, and places past kScatterPlaces are read one by one
+// again: 2000 x 20 of 2048 30 / 38.
+bool quantize_scatters(int64_t T, int64_t src_rows, int64_t K) {
+    return K >= 512 && T <= kScatterPlaces * src_rows && (T - src_rows) >= (2 << 20) / K;
+}
+// Its workspace: counts (to 16 bytes), places, more.
+int64_t scatter_taken(int64_t src_rows) { return cdiv(src_rows + 1, 4) * 4; }
+
 template <int FMT>
-void launch_quantize_grouped(const GroupedQuantParams &p, int64_t bands, cudaStream_t st) {
+void launch_quantize_scatter(GroupedQuantParams &p, int64_t bands, cudaStream_t st) {
+    cudaLaunchAttribute attr[1];
+    const int64_t n = p.src_rows + 1;
+    cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)cdiv(n, 256), 1, 1), 256, 0, st, attr);
+    cudaLaunchKernelEx(&cfg, scatter_zero_kernel, p.taken, n);
+    cfg = launch_cfg(dim3((unsigned)bands, 1, 1), 128, 0, st, attr);
+    cudaLaunchKernelEx(&cfg, scatter_link_kernel<FMT != FMT_B128>, p);
+    // few rows: several warps per row, down to 1024 columns each
+    const int64_t most = cdiv(p.K, 1024), want = cdiv(32 * (int64_t)num_sms(), p.src_rows);
+    p.slab = (int)(cdiv(cdiv(p.K, want < most ? want : most), 1024) * 1024);
+    p.slabs = (int)cdiv(p.K, p.slab);
+    p.row_ctas = (int)cdiv(p.src_rows * p.slabs, kQThreads / 32);
+    cfg = launch_cfg(dim3((unsigned)(p.row_ctas + num_sms()), 1, 1), kQThreads, 0, st, attr);
+    cudaLaunchKernelEx(&cfg, quantize_scatter_kernel<FMT>, p);
+}
+
+template <int FMT>
+void launch_quantize_grouped(GroupedQuantParams &p, int64_t bands, cudaStream_t st) {
+    if (p.taken != nullptr) return launch_quantize_scatter<FMT>(p, bands, st);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)(bands * p.slabs), 1, 1), kQThreads, 0, st, attr);
     cudaLaunchKernelEx(&cfg, quantize_grouped_kernel<FMT>, p);
@@ -258,9 +289,15 @@ size_t mx_grouped_scales_bytes(int fmt, int64_t rows, int64_t groups, int64_t co
     return scales_bytes(fmt, group_bands(rows, groups) * 128, cols);
 }
 
+size_t mx_quantize_grouped_workspace_bytes(int64_t rows, int64_t src_rows, int64_t K) {
+    if (rows < 0 || src_rows < 0 || K < 0 || rows > INT32_MAX || src_rows > INT32_MAX) return 0;
+    if (!quantize_scatters(rows, src_rows, K)) return 0;
+    return (size_t)(4 * scatter_taken(src_rows) + 8 * kScatterPlaces * src_rows + 16 * rows);
+}
+
 mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, int64_t K, int64_t ld_src,
                               const int32_t *row_index, const mx_groups *groups, mx_tensor *dst,
-                              const float *gscale_in, void *stream) {
+                              const float *gscale_in, void *workspace, size_t workspace_bytes, void *stream) {
     if (!valid_fmt_any(fmt) || fmt == MX_MXFP4_MBS || fmt == MX_FP8_B128X128 || !dst || src_rows < 0 || K < 0)
         return MX_ERR_INVALID_ARG;
     mx_status s = check_groups(groups);
@@ -275,6 +312,9 @@ mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, i
     if (ld_src < K || (ld_src & 7) != 0) return MX_ERR_MISALIGNED;
     if (!aligned16(src_bf16) || !aligned16(dst->codes) || !aligned16(dst->scales)) return MX_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(row_index) & 3u) != 0) return MX_ERR_MISALIGNED;
+    const size_t need = row_index && workspace ? mx_quantize_grouped_workspace_bytes(T, src_rows, K) : 0;
+    if (workspace_bytes < need) return MX_ERR_INVALID_ARG;
+    if (need > 0 && !aligned16(workspace)) return MX_ERR_MISALIGNED;
     const int64_t bands = group_bands(T, groups->count), tiles = cdiv(K, kQTileCols);
     if (T > INT32_MAX || src_rows > INT32_MAX || bands * tiles > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -296,6 +336,11 @@ mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, i
     if (p.slab > 4) p.slab = 4;
     if (p.slab < 1) p.slab = 1;
     p.slabs = (int)cdiv(tiles, p.slab);
+    if (need > 0) {
+        p.taken = static_cast<int32_t *>(workspace);
+        p.places = reinterpret_cast<int2 *>(p.taken + scatter_taken(src_rows));
+        p.more = reinterpret_cast<int4 *>(p.places + kScatterPlaces * src_rows);
+    }
     switch (fmt) {
     case MX_FP8_B128: launch_quantize_grouped<FMT_B128>(p, bands, st); break;
     case MX_MXFP8_E4M3: launch_quantize_grouped<FMT_E4M3>(p, bands, st); break;

@@ -197,48 +197,90 @@ struct GroupedQuantParams {
     uint8_t *scales;             // 128-row tiles, or FP8_B128's floats
     int64_t sf_tiles_k;
     int64_t pitch;               // FP8_B128: floats per K block
-    int slab, slabs;             // K tiles per CTA, CTAs per band
+    int slab, slabs;             // K tiles per CTA, CTAs per band; scatter: columns per warp, warps per row
     const float *gscale;         // NVFP4: g
     float *gscale_out;           // NVFP4, nullable: receives g
+    // scatter: the rows of dst that each row of src goes to
+    int32_t *taken;              // [src_rows + 1]: how many, and (last) the length of more
+    int2 *places;                // [src_rows][kScatterPlaces]: (row of dst, row of the scale buffer)
+    int4 *more;                  // [T]: places past those, and rows of zeros: (as above, row of src or -1, 0)
+    int row_ctas;                // CTAs of the rows of src; the others take `more`
 };
 
-// Codes of 16 values (v0, v1) of row `row`, columns col .. col + 15, stored where
-// `ok`, and their block's scale byte, returned: the arithmetic of
+// Codes of 16 values (v0, v1), packed as they are stored (4, 3 or 2 words of 8-,
+// 6- or 4-bit codes), and their block's scale byte, returned: the arithmetic of
 // quantize_seg16.  (A function of its own: shared with quantize_seg16, it made
 // the plain kernels 10% slower.)  A 32-element block spans lanes lane and
 // lane ^ 1, which call together.
 template <int FMT>
-MX_DEVICE_INLINE uint32_t quantize_codes16(const uint4 &v0, const uint4 &v1, int64_t row, bool ok, int64_t col,
-                                           int64_t K, const NvScale &ns, const NvTables *__restrict__ nvt,
-                                           uint8_t *__restrict__ codes) {
+MX_DEVICE_INLINE uint32_t quantize_codes16(const uint4 &v0, const uint4 &v1, const NvScale &ns,
+                                           const NvTables *__restrict__ nvt, uint32_t (&q)[4]) {
     uint32_t m = absmax16(v0, v1);
     if constexpr (FMT == FMT_NVFP4) {
         const uint32_t sbyte = nv_block_scale(__uint_as_float(m << 16) * ns.sc, ns.g, ns.inv6g, nvt->val);
-        if (ok) {
-            uint32_t q0, q1;
-            const float r_lo = __fmul_rd(ns.rg_lo, nvt->inv_lo[sbyte]);
-            const float r_hi = __fmul_ru(ns.rg_hi, nvt->inv_hi[sbyte]);
-            nv_codes16(v0, v1, ns.g, nvt->val[sbyte], r_lo, r_hi, q0, q1, ns.sc);
-            *reinterpret_cast<uint2 *>(codes + row * (K / 2) + col / 2) = make_uint2(q0, q1);
-        }
+        const float r_lo = __fmul_rd(ns.rg_lo, nvt->inv_lo[sbyte]);
+        const float r_hi = __fmul_ru(ns.rg_hi, nvt->inv_hi[sbyte]);
+        nv_codes16(v0, v1, ns.g, nvt->val[sbyte], r_lo, r_hi, q[0], q[1], ns.sc);
         return sbyte;
     } else {
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const int E = mx_scale_byte<FMT, RULE_OCP>(m);
-        if (ok) {
-            const float inv = mx_inv_scale(E);
-            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-            float f[16];
+        const float inv = mx_inv_scale(E);
+        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        float f[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[2 * e] = bf16lo(w[e]) * inv;
-                f[2 * e + 1] = bf16hi(w[e]) * inv;
-            }
-            store_mx_codes16<FMT>(codes, row, K, col, f);
+        for (int e = 0; e < 8; ++e) {
+            f[2 * e] = bf16lo(w[e]) * inv;
+            f[2 * e + 1] = bf16hi(w[e]) * inv;
+        }
+        if constexpr (FmtTraits<FMT>::kBits == 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = cvt4_fp8<FMT>(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+        } else if constexpr (FmtTraits<FMT>::kBits == 6) {
+            uint32_t t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = pack4x6(cvt4_e3m2(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
+            q[0] = t[0] | (t[1] << 24);
+            q[1] = (t[1] >> 8) | (t[2] << 16);
+            q[2] = (t[2] >> 16) | (t[3] << 8);
+        } else {
+            q[0] = cvt8_e2m1(reinterpret_cast<const float(&)[8]>(f[0]));
+            q[1] = cvt8_e2m1(reinterpret_cast<const float(&)[8]>(f[8]));
         }
         return (uint32_t)E;
     }
 }
+
+// The packed codes to their place: columns col .. col + 15 of a row.
+template <int BITS>
+MX_DEVICE_INLINE void put_codes16(uint8_t *__restrict__ codes, int64_t row, int64_t K, int64_t col, const uint32_t (&q)[4]) {
+    uint8_t *dst = codes + row * (K / 8 * BITS) + col / 8 * BITS;
+    if (BITS == 8) {
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+    } else if (BITS == 6) {   // 12 bytes at a 4-byte aligned offset
+#pragma unroll
+        for (int e = 0; e < 3; ++e) reinterpret_cast<uint32_t *>(dst)[e] = q[e];
+    } else {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
+    }
+}
+
+// The four scale bytes that share a word of a 512-byte chunk (one row's; 32-element
+// blocks: all of a 128-column tile's, 16-element blocks: half of them), from the
+// lanes' bytes to the lane that stores the word: l8 & scale_word_mask == 0.
+template <int FMT>
+MX_DEVICE_INLINE uint32_t scale_word(uint32_t byte, int l8) {
+    constexpr bool k16 = FmtTraits<FMT>::kBlock == 16;
+    uint32_t w = k16 || (l8 & 1) == 0 ? byte << (8 * (k16 ? l8 & 3 : l8 >> 1)) : 0u;
+    if (k16) w |= __shfl_xor_sync(0xffffffffu, w, 1);
+    w |= __shfl_xor_sync(0xffffffffu, w, 2);
+    if (!k16) w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    return w;
+}
+template <int FMT>
+constexpr int scale_word_mask = FmtTraits<FMT>::kBlock == 16 ? 3 : 7;
+// Byte of row r's word within a chunk.
+MX_DEVICE_INLINE int scale_word_at(int r) { return (r & 31) * 16 + (r >> 5) * 4; }
 
 constexpr int FMT_B128 = 6;
 
@@ -320,22 +362,165 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_grouped_kernel(GroupedQ
                     }
                 }
             } else {
-                // the four scale bytes of a row in one 512-byte chunk (32-element
-                // blocks: all of the tile's; 16-element blocks: half of them)
                 constexpr bool k16 = FmtTraits<FMT>::kBlock == 16;
                 uint32_t w = 0u;
                 if (i < passes) {
-                    w = quantize_codes16<FMT>(v[i][0], v[i][1], row, ok, col, p.K, ns, &nvt, p.codes);
-                    w = ok && (k16 || (lane & 1) == 0) ? w << (8 * (k16 ? l8 & 3 : l8 >> 1)) : 0u;
-                    if (k16) w |= __shfl_xor_sync(0xffffffffu, w, 1);
-                    w |= __shfl_xor_sync(0xffffffffu, w, 2);
-                    if (!k16) w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                    uint32_t q[4];
+                    if (FMT != FMT_NVFP4 || ok) w = quantize_codes16<FMT>(v[i][0], v[i][1], ns, &nvt, q);
+                    if (ok) put_codes16<FmtTraits<FMT>::kBits>(p.codes, row, p.K, col, q);
+                    w = scale_word<FMT>(ok ? w : 0u, l8);
                 }
                 const int64_t chunk = k16 ? 2 * (int64_t)t + (l8 >> 2) : t;
-                if ((k16 ? l8 & 3 : l8) == 0 && chunk < p.sf_tiles_k)
-                    *reinterpret_cast<uint32_t *>(p.scales + (band * p.sf_tiles_k + chunk) * 512 + (rl & 31) * 16 +
-                                                  (rl >> 5) * 4) = w;
+                if ((l8 & scale_word_mask<FMT>) == 0 && chunk < p.sf_tiles_k)
+                    *reinterpret_cast<uint32_t *>(p.scales + (band * p.sf_tiles_k + chunk) * 512 + scale_word_at(rl)) = w;
             }
+        }
+    }
+}
+
+// The same by source row, for rows that go to several groups: a row is read and
+// quantized once and its codes stored at all its places, where the gather reads
+// and quantizes it once per place.  First the places are turned round:
+// scatter_link_kernel, a CTA per band, enters each row of dst with its source
+// (the order within a source's list varies from run to run; what is stored does
+// not depend on it) and writes the zero scales of the bands' rows past their
+// group.  Bound by HBM and by what the SMs keep in flight between the stores of
+// one row and the loads of the next: 16384 tokens x 4 choices (a tenth of them
+// padding) x 4096 to FP8_B128 79 us (128 by destination; 376 MB at the copy's
+// rate 57), to NVFP4 69 (157); one or four pieces of 512 columns in flight 84
+// and 82.
+constexpr int kScatterPlaces = 8;
+
+__global__ void __launch_bounds__(256) scatter_zero_kernel(int32_t *taken, int64_t n) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) taken[i] = 0;
+}
+
+template <bool BANDED>
+__global__ void __launch_bounds__(128) scatter_link_kernel(GroupedQuantParams p) {
+    __shared__ int rows_of[2];
+    const int lane = threadIdx.x & 31;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (threadIdx.x < 32) {
+        int r0 = 0, r1 = 0;
+        GroupWalk walk(p.groups, 7, lane);
+        GroupBlock g;
+        if (walk.find((int)blockIdx.x, g)) {
+            r0 = g.start + ((int)blockIdx.x - g.first) * kQTileRows;
+            r1 = min(g.end, r0 + kQTileRows);
+        }
+        if (lane == 0) {
+            rows_of[0] = r0;
+            rows_of[1] = r1;
+        }
+    }
+    __syncthreads();
+    const int row0 = rows_of[0], n = rows_of[1] - row0;
+    if ((int)threadIdx.x < n) {
+        const int row = row0 + (int)threadIdx.x, srow = (int)blockIdx.x * kQTileRows + (int)threadIdx.x;
+        const int64_t src = p.row_index[row];
+        const bool real = src >= 0 && src < p.src_rows;
+        const int at = real ? atomicAdd(&p.taken[src], 1) : kScatterPlaces;
+        if (at < kScatterPlaces)
+            p.places[src * kScatterPlaces + at] = make_int2(row, srow);
+        else {
+            const int e = atomicAdd(&p.taken[p.src_rows], 1);
+            if (e < p.groups.rows) p.more[e] = make_int4(row, srow, real ? (int)src : -1, 0);   // (offsets that descend
+        }                                                                                       // enter rows twice)
+    }
+    if (BANDED && n < kQTileRows) {
+        const int word = threadIdx.x, r = (word >> 2) + 32 * (word & 3);   // word of a chunk, its row
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.scales) + (int64_t)blockIdx.x * p.sf_tiles_k * 128 + word;
+        if (r >= n)
+            for (int64_t c = 0; c < p.sf_tiles_k; ++c) dst[c * 128] = 0u;
+    }
+}
+
+// One warp per row of src (or p.slab columns of it), 512 columns at a time (8 lanes per 128 as above), two
+// of those in flight.
+template <int FMT>
+__global__ void __launch_bounds__(kQThreads, 4) quantize_scatter_kernel(GroupedQuantParams p) {
+    constexpr int kWarps = kQThreads / 32, kAhead = 2, kCols = 512;
+    __shared__ NvTables nvt;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l8 = lane & 7;
+    griddep_wait();
+    griddep_launch_dependents();
+    NvScale ns{1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if (FMT == FMT_NVFP4) {
+        const float g = *p.gscale;
+        if (p.gscale_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.gscale_out = g;
+        ns = nv_scale_setup(g);
+        if (threadIdx.x < 128) nv_tables_fill(&nvt, threadIdx.x);
+        __syncthreads();
+    }
+    // one row of src (-1: zeros) to n places, held by the lanes
+    auto row_to = [&](int64_t src, int n, int place, int srow, int64_t begin, int64_t end) {
+        const uint16_t *row = p.src + src * p.ld;
+        for (int64_t c0 = begin + lane * 16; c0 - lane * 16 < end; c0 += kAhead * kCols) {
+            uint4 v[kAhead][2];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t col = c0 + i * kCols;
+                v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (src >= 0 && col < p.K) {
+                    v[i][0] = ldg_stream(row + col);
+                    v[i][1] = ldg_stream(row + col + 8);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t col = c0 + i * kCols, tile = col / kQTileCols;
+                const bool ok = col < p.K;
+                if constexpr (FMT == FMT_B128) {
+                    uint32_t m = absmax16(v[i][0], v[i][1]);
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    const B128Scale b = b128_scale(m);
+                    const uint4 q = b128_codes16(v[i][0], v[i][1], b);
+                    for (int j = 0; j < n; ++j) {
+                        const int64_t to = __shfl_sync(0xffffffffu, place, j);
+                        if (ok) {
+                            *reinterpret_cast<uint4 *>(p.codes + to * p.K + col) = q;
+                            if (l8 == 0) reinterpret_cast<float *>(p.scales)[tile * p.pitch + to] = b.s;
+                        }
+                    }
+                } else {
+                    constexpr bool k16 = FmtTraits<FMT>::kBlock == 16;
+                    uint32_t q[4];
+                    const uint32_t byte = quantize_codes16<FMT>(v[i][0], v[i][1], ns, &nvt, q);
+                    const uint32_t w = scale_word<FMT>(ok ? byte : 0u, l8);
+                    const int64_t chunk = k16 ? 2 * tile + (l8 >> 2) : tile;
+                    const bool stores = (l8 & scale_word_mask<FMT>) == 0 && chunk < p.sf_tiles_k;
+                    for (int j = 0; j < n; ++j) {
+                        const int64_t to = __shfl_sync(0xffffffffu, place, j);
+                        const int sr = __shfl_sync(0xffffffffu, srow, j);
+                        if (ok) put_codes16<FmtTraits<FMT>::kBits>(p.codes, to, p.K, col, q);
+                        if (stores)
+                            *reinterpret_cast<uint32_t *>(p.scales + ((sr >> 7) * p.sf_tiles_k + chunk) * 512 +
+                                                          scale_word_at(sr & 127)) = w;
+                    }
+                }
+            }
+        }
+    };
+    if ((int)blockIdx.x < p.row_ctas) {
+        const int64_t unit = (int64_t)blockIdx.x * kWarps + warp, src = unit / p.slabs;
+        const int64_t begin = (unit - src * p.slabs) * p.slab;
+        if (src >= p.src_rows) return;
+        const int n = min(p.taken[src], kScatterPlaces);
+        int2 at = make_int2(0, 0);
+        if (lane < n) at = p.places[src * kScatterPlaces + lane];
+        if (n > 0) row_to(src, n, at.x, at.y, begin, min(begin + p.slab, p.K));
+    } else {
+        const int first = ((int)blockIdx.x - p.row_ctas) * kWarps + warp, step = ((int)gridDim.x - p.row_ctas) * kWarps;
+        const int count = min(p.taken[p.src_rows], p.groups.rows);
+        for (int e = first; e < count; e += step) {
+            const int4 at = p.more[e];
+            row_to(at.z, 1, at.x, at.y, 0, p.K);
         }
     }
 }

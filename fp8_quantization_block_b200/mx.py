@@ -43,7 +43,7 @@ EXPORTED = [
     "mx_version", "mx_debug_set", "mx_gemm_fused_act_noalloc", "mx_quantize_oas", "mx_qsnr",
     "mx_quantize_rht", "mx_quantize_mbs_dynamic", "mx_fused_split_workspace_bytes", "mx_debug_split_units",
     "mx_route_workspace_bytes", "mx_route", "mx_grouped_scales_bytes", "mx_quantize_grouped", "mx_gemm_grouped",
-    "mx_combine",
+    "mx_combine", "mx_quantize_grouped_workspace_bytes",
 ]
 MX_MAX_GROUPS = 1024
 MX_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -104,7 +104,8 @@ def lib() -> ctypes.CDLL:
                 "mx_route_workspace_bytes": (sz, [i64, i32, i32]),
                 "mx_route": (i32, [P, i32, i64, i32, i32, P, P, P, P, sz, P]),
                 "mx_grouped_scales_bytes": (sz, [i32, i64, i64, i64]),
-                "mx_quantize_grouped": (i32, [i32, P, i64, i64, i64, P, G, T, P, P]),
+                "mx_quantize_grouped_workspace_bytes": (sz, [i64, i64, i64]),
+                "mx_quantize_grouped": (i32, [i32, P, i64, i64, i64, P, G, T, P, P, sz, P]),
                 "mx_gemm_grouped": (i32, [T, T, G, P, i64, i32, P]),
                 "mx_combine": (i32, [P, i64, i64, i64, P, P, i64, i32, P, i64, P]),
             }
@@ -209,10 +210,15 @@ def mx_grouped_scales_bytes(fmt: int, rows: int, groups: int, cols: int) -> int:
     return int(lib().mx_grouped_scales_bytes(fmt, rows, groups, cols))
 
 
+@functools.lru_cache(maxsize=4096)
+def mx_quantize_grouped_workspace_bytes(rows: int, src_rows: int, K: int) -> int:
+    return int(lib().mx_quantize_grouped_workspace_bytes(rows, src_rows, K))
+
+
 def mx_quantize_grouped(fmt, src_ptr, src_rows, K, ld, row_index_ptr, groups: MxGroupsC, dst: MxTensorC, gscale_in_ptr,
-                        stream) -> int:
+                        ws_ptr, ws_bytes, stream) -> int:
     return int(lib().mx_quantize_grouped(fmt, src_ptr, src_rows, K, ld, row_index_ptr, ctypes.byref(groups),
-                                         ctypes.byref(dst), gscale_in_ptr, stream))
+                                         ctypes.byref(dst), gscale_in_ptr, ws_ptr, ws_bytes, stream))
 
 
 def mx_gemm_grouped(A: MxTensorC, B: MxTensorC, groups: MxGroupsC, C_ptr, ldc, epilogue, stream) -> int:
@@ -478,13 +484,14 @@ def _nbytes(t: torch.Tensor) -> int:
 
 
 def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, row_index: torch.Tensor | None = None,
-                     gscale: torch.Tensor | None = None, out: MxTensor | None = None, stream=None) -> MxTensor:
+                     gscale: torch.Tensor | None = None, out: MxTensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> MxTensor:
     """Rows of x (x[row_index[t]], or x itself) quantized for gemm_grouped.  NVFP4 wants gscale (g)."""
     _rows_ok(x, "x")
     groups = _groups(offsets)
     if (ctx := _elsewhere(x, stream)) is not None:
         with ctx:
-            return quantize_grouped(x, offsets, fmt, row_index, gscale, out)
+            return quantize_grouped(x, offsets, fmt, row_index, gscale, out, workspace)
     K = x.shape[1]
     if row_index is not None:
         _need(row_index.dtype == torch.int32 and row_index.dim() == 1 and row_index.is_contiguous(),
@@ -496,9 +503,14 @@ def quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, fmt: int, row_index
         _need(out.fmt == fmt and out.rows == rows and out.cols == K, "out: another format or size")
         _need(_nbytes(out.codes) >= mx_codes_bytes(fmt, rows, K) and
               _nbytes(out.scales) >= mx_grouped_scales_bytes(fmt, rows, groups.count, K), "out: a buffer is too small")
-    _same_device(x, offsets, row_index, gscale, out.codes, out.scales, out.gscale)
+    if workspace is None and row_index is not None:
+        need = mx_quantize_grouped_workspace_bytes(rows, x.shape[0], K)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _same_device(x, offsets, row_index, gscale, out.codes, out.scales, out.gscale, workspace)
     check(mx_quantize_grouped(fmt, x.data_ptr(), x.shape[0], K, _pitch(x), _ptr(row_index), groups, out.c(), _ptr(gscale),
-                              _stream(stream)), "mx_quantize_grouped")
+                              _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(stream)),
+          "mx_quantize_grouped")
     return out
 
 

@@ -359,11 +359,16 @@ mx_status mx_route(const void *ids, int id_bits, int64_t tokens, int choices, in
  *   r of group g is row 128 * (sum of ceil(rows / 128) over the groups before
  *   g) + r of the tiled layout; all other bytes are 0.
  * NVFP4: gscale_in (not NULL) is the device float g.  Formats: all that
- * mx_gemm_grouped takes for A.  T < 2^31. */
+ * mx_gemm_grouped takes for A.  T < 2^31.
+ * workspace: device, 16-byte aligned, mx_quantize_grouped_workspace_bytes bytes
+ * (0: not used), scratch, not to be shared by calls that overlap on the GPU.
+ * With it, rows that row_index names several times are read once; NULL will do
+ * (the same result, more slowly). */
+size_t mx_quantize_grouped_workspace_bytes(int64_t rows, int64_t src_rows, int64_t K);
 size_t mx_grouped_scales_bytes(int fmt, int64_t rows, int64_t groups, int64_t cols);
 mx_status mx_quantize_grouped(int fmt, const void *src_bf16, int64_t src_rows, int64_t K, int64_t ld_src,
                               const int32_t *row_index, const mx_groups *groups, mx_tensor *dst,
-                              const float *gscale_in, void *stream);
+                              const float *gscale_in, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The experts' products:
  *   C[t][j] = RNE_bf16(f(sum_k A_dq[t][k] * B_g,dq[j][k]))  for every row t of group g,

@@ -71,7 +71,7 @@ def test_block128_calls_refuse():
 
 def test_quantize_grouped_refuses():
     def q(fmt=6, src=0x1000, src_rows=9, K=256, ld=256, idx=0x7000, groups=None, dst=None, g=0x9000):
-        return mx.mx_quantize_grouped(fmt, src, src_rows, K, ld, idx, groups or G(), dst or T(fmt, 9, K), g, None)
+        return mx.mx_quantize_grouped(fmt, src, src_rows, K, ld, idx, groups or G(), dst or T(fmt, 9, K), g, None, 0, None)
     assert q(fmt=5) == BAD and q(fmt=8) == BAD and q(fmt=7) == BAD
     assert q(groups=G(0)) == BAD and q(groups=G(4, None)) == BAD and q(groups=G(1025)) == SHAPE
     assert q(groups=G(4, 0x8002)) == ALIGN and q(idx=0x7001) == ALIGN
@@ -81,6 +81,16 @@ def test_quantize_grouped_refuses():
     assert q(ld=255) == ALIGN and q(src=0x1008) == ALIGN and q(src=None) == BAD
     assert q(fmt=3, g=None) == BAD
     assert q(dst=T(6, 0, 256)) == OK                   # no rows: nothing to do
+    # the workspace of rows that go to several places
+    need = mx.mx_quantize_grouped_workspace_bytes(4096, 1024, 1024)
+    assert need >= 4 * 1025 + 64 * 1024 + 16 * 4096
+    for rows, src in ((1024, 1024), (32 * 8, 32), (20 * 1024, 1024), (-1, 4), (4, -1)):
+        assert mx.mx_quantize_grouped_workspace_bytes(rows, src, 1024) == 0
+    assert mx.mx_quantize_grouped_workspace_bytes(4096, 1024, 384) == 0
+    assert mx.mx_quantize_grouped_workspace_bytes(4096, 1024, 0) == 0
+    def w(ws, n):  # noqa: E306
+        return mx.mx_quantize_grouped(6, 0x1000, 1024, 1024, 1024, 0x7000, G(), T(6, 4096, 1024), None, ws, n, None)
+    assert w(0x20000, need - 1) == BAD and w(0x20008, need) == ALIGN
 
 
 def test_gemm_grouped_refuses():

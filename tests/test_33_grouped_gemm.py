@@ -252,3 +252,75 @@ def test_a_stalled_producer_is_reported(fa, fb):
     assert mx.mx_check_device_error()[0] == mx.MX_OK
     assert torch.equal(mx.gemm_grouped(a, w, od), c)
     assert mx.mx_check_device_error()[0] == mx.MX_OK
+
+
+def scattered(seed, tokens, T, how):
+    g = torch.Generator().manual_seed(seed)
+    if how == "one":
+        idx = torch.full((T,), 3)
+    elif how == "outside":
+        idx = torch.randint(-tokens, 2 * tokens, (T,), generator=g)
+        idx[0], idx[1] = -2 ** 31, 2 ** 31 - 1
+    else:
+        idx = torch.randint(0, tokens, (T,), generator=g)
+    return idx.int().cuda()
+
+
+@pytest.mark.parametrize("fmt", [6, 0, 1, 2, 3, 4])
+@pytest.mark.parametrize("tokens,T,K,how", [(700, 2100, 2048, "random"), (600, 4800, 640, "random"), (300, 1500, 4096, "one"),
+                                            (400, 2000, 1536, "outside"), (300, 2400, 1152, "random")])
+def test_rows_to_several_places(fmt, tokens, T, K, how):
+    """Read once and stored at every place (a workspace given), or gathered place by place: the same bytes."""
+    counts = [T // 3, 0, 1, T // 2, 100]
+    o, od = offsets_of(counts)
+    x = torch.full((tokens, K + 8), 5.0, dtype=torch.bfloat16, device="cuda")[:, :K]
+    x.copy_(activations(K, tokens, K))
+    idx = scattered(T, tokens, T, how)
+    need = mx.mx_quantize_grouped_workspace_bytes(T, tokens, K)
+    assert need > 0
+    got, want = (mx.empty_grouped(fmt, T, len(counts), K) for _ in range(2))
+    for t in (got, want):
+        t.codes.fill_(0xA5)
+        t.scales.fill_(0x5A)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):                                  # a used workspace is as good as a new one
+        mx.quantize_grouped(x, od, fmt, row_index=idx, gscale=gs(fmt), out=got, workspace=ws)
+    groups = mx.MxGroupsC(len(counts), 0, od.data_ptr())
+    g = gs(fmt)
+    mx.check(mx.mx_quantize_grouped(fmt, x.data_ptr(), tokens, K, K + 8, idx.data_ptr(), groups, want.c(),
+                                    None if g is None else g.data_ptr(), None, 0, mx._stream()))
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    if g is not None:
+        assert torch.equal(got.gscale, g)
+    # and the codes are those of the rows themselves
+    live = idx[:o[-1]].long()
+    rows = torch.where(((live >= 0) & (live < tokens))[:, None], x[live.clamp(0, tokens - 1)], 0)
+    q = mx.quantize(rows.contiguous(), fmt, gscale=g)
+    n = mx.mx_codes_bytes(fmt, o[-1], K)
+    assert torch.equal(got.codes[:n], q.codes[:n]) and (got.codes[n:] == 0xA5).all()
+
+
+def test_rows_to_several_places_in_two_graphs_at_once():
+    """Two captured calls have workspaces of their own and run together."""
+    T, tokens, K, E = 4096, 1024, 2048, 16
+    cases = []
+    for seed in (1, 2):
+        x = activations(seed, tokens, K)
+        ids = torch.randint(0, E, (tokens, 4), generator=torch.Generator().manual_seed(seed)).int().cuda()
+        r = mx.route(ids, E)
+        want = mx.quantize_grouped(x, r.offsets, 6, row_index=r.row_token)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = [mx.quantize_grouped(x, r.offsets, 6, row_index=r.row_token) for _ in range(4)]
+        cases.append((s, g, got, want, x, r))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, g, *_ in cases:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, _, got, want, *_ in cases:
+        for t in got:
+            assert torch.equal(t.codes, want.codes) and torch.equal(t.scales, want.scales)
