@@ -177,7 +177,7 @@ mx_status check_groups(const mx_groups *g) {
 // rows that the gather would read again are worth two more launches.  us by
 // destination / by source, FP8_B128: 32 x 8 places of 4096 columns 5.2 / 6.1,
 // 64 x 8 6.1 / 6.3, 4096 x 4 of 512 8.4 / 7.2, 1024 x 2 of 4096 8.5 / 6.7,
-// 256 x 8 12.8 / 7.4, 1024 x 8 24.4 / 12.1, 16384 x 4 130 / 79.  A warp takes
+// 256 x 8 12.8 / 7.4, 1024 x 8 24.7 / 12.5, 16384 x 4 129 / 66.  A warp takes
 // 512 columns at once, and places past kScatterPlaces are read one by one
 // again: 2000 x 20 of 2048 30 / 38.
 bool quantize_scatters(int64_t T, int64_t src_rows, int64_t K) {
@@ -194,8 +194,11 @@ void launch_quantize_scatter(GroupedQuantParams &p, int64_t bands, cudaStream_t 
     cudaLaunchKernelEx(&cfg, scatter_zero_kernel, p.taken, n);
     cfg = launch_cfg(dim3((unsigned)bands, 1, 1), 128, 0, st, attr);
     cudaLaunchKernelEx(&cfg, scatter_link_kernel<FMT != FMT_B128>, p);
-    // few rows: several warps per row, down to 1024 columns each
-    const int64_t most = cdiv(p.K, 1024), want = cdiv(32 * (int64_t)num_sms(), p.src_rows);
+    // Columns of a row in pieces of 1024 or more to several warps, up to 256
+    // warps per SM in all: neighbouring pieces are then stored together (16384 x
+    // 4 x 4096: 66 us, 71 with whole rows; 1024 x 8: 12.3, 14.8), and more CTAs
+    // than that cost NVFP4 its tables' filling (67, 72 in pieces of 1024).
+    const int64_t most = cdiv(p.K, 1024), want = cdiv(256 * (int64_t)num_sms(), p.src_rows);
     p.slab = (int)(cdiv(cdiv(p.K, want < most ? want : most), 1024) * 1024);
     p.slabs = (int)cdiv(p.K, p.slab);
     p.row_ctas = (int)cdiv(p.src_rows * p.slabs, kQThreads / 32);

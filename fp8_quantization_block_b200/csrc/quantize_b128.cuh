@@ -251,17 +251,20 @@ MX_DEVICE_INLINE uint32_t quantize_codes16(const uint4 &v0, const uint4 &v1, con
     }
 }
 
-// The packed codes to their place: columns col .. col + 15 of a row.
+// The packed codes to their place: columns col .. col + 15 of a row.  Stored
+// streaming, so that the codes leave the cache's room to the source rows
+// (16384 x 4 x 4096 by source row: 75 us without, 65 with; a grouped GEMM that
+// follows takes the same time, 8 to 32 MB of codes).
 template <int BITS>
 MX_DEVICE_INLINE void put_codes16(uint8_t *__restrict__ codes, int64_t row, int64_t K, int64_t col, const uint32_t (&q)[4]) {
     uint8_t *dst = codes + row * (K / 8 * BITS) + col / 8 * BITS;
     if (BITS == 8) {
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+        __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(q[0], q[1], q[2], q[3]));
     } else if (BITS == 6) {   // 12 bytes at a 4-byte aligned offset
 #pragma unroll
-        for (int e = 0; e < 3; ++e) reinterpret_cast<uint32_t *>(dst)[e] = q[e];
+        for (int e = 0; e < 3; ++e) __stcs(reinterpret_cast<uint32_t *>(dst) + e, q[e]);
     } else {
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
+        __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(q[0], q[1]));
     }
 }
 
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_grouped_kernel(GroupedQ
                     m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     const B128Scale b = b128_scale(m);
                     if (ok) {
-                        *reinterpret_cast<uint4 *>(p.codes + row * p.K + col) = b128_codes16(v[i][0], v[i][1], b);
+                        __stcs(reinterpret_cast<uint4 *>(p.codes + row * p.K + col), b128_codes16(v[i][0], v[i][1], b));
                         if (l8 == 0) reinterpret_cast<float *>(p.scales)[t * p.pitch + row] = b.s;
                     }
                 }
@@ -384,11 +387,9 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_grouped_kernel(GroupedQ
 // scatter_link_kernel, a CTA per band, enters each row of dst with its source
 // (the order within a source's list varies from run to run; what is stored does
 // not depend on it) and writes the zero scales of the bands' rows past their
-// group.  Bound by HBM and by what the SMs keep in flight between the stores of
-// one row and the loads of the next: 16384 tokens x 4 choices (a tenth of them
-// padding) x 4096 to FP8_B128 79 us (128 by destination; 376 MB at the copy's
-// rate 57), to NVFP4 69 (157); one or four pieces of 512 columns in flight 84
-// and 82.
+// group.  Bound by HBM: 16384 tokens x 4 choices (a tenth of them padding) x
+// 4096 to FP8_B128 66 us, 5.7 TB/s (129 by destination), to NVFP4 67 (157).
+// One or four pieces of 512 columns in flight per warp: 6% and 3% slower.
 constexpr int kScatterPlaces = 8;
 
 __global__ void __launch_bounds__(256) scatter_zero_kernel(int32_t *taken, int64_t n) {
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_scatter_kernel(GroupedQ
                     for (int j = 0; j < n; ++j) {
                         const int64_t to = __shfl_sync(0xffffffffu, place, j);
                         if (ok) {
-                            *reinterpret_cast<uint4 *>(p.codes + to * p.K + col) = q;
+                            __stcs(reinterpret_cast<uint4 *>(p.codes + to * p.K + col), q);
                             if (l8 == 0) reinterpret_cast<float *>(p.scales)[tile * p.pitch + to] = b.s;
                         }
                     }
