@@ -10,7 +10,8 @@
 // shared counters in the placing step, so the order never varies: every warp
 // owns a contiguous run of choices, counts it per expert, takes the counts of
 // the warps before it as its bases, and then places 32 choices at a time, the
-// rank within the 32 from __match_any_sync.
+// rank within the 32 from __match_any_sync.  Bound by latency, not bytes: 256
+// choices of 64 experts 2.8 us, 65536 of 128 7.7 us (0.8 MB).
 //
 // Combine: out[t] = RNE_bf16(sum_j w[t][j] Y[slot[t][j]]), FP32, j ascending.
 #pragma once
@@ -23,11 +24,13 @@ namespace mx {
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxGroups = 1024;
-// Choices per CTA: 2048 (one CTA alone up to there), more where that would make
-// over 128 CTAs, each of which adds up the counts of all the others.
+// Choices per CTA: one CTA alone up to 2048 (5.2 us; two of 1024 with the second
+// kernel 6.8), else 1024 (8192 choices: 7.2 us, 10.4 in pieces of 2048), and
+// more where that would make over 64 CTAs, each of which adds up the counts of
+// all the others (131072 choices: 12.3 us, 15.8 in 128 pieces).
 inline int64_t route_chunk(int64_t n) {
-    const int64_t per = (n + 127) / 128, unit = 32 * kRouteWarps;
-    return per <= 2048 ? 2048 : (per + unit - 1) / unit * unit;
+    const int64_t per = (n + 63) / 64, unit = 32 * kRouteWarps;
+    return n <= 2048 ? 2048 : (per <= 1024 ? 1024 : (per + unit - 1) / unit * unit);
 }
 
 struct RouteParams {
@@ -48,6 +51,14 @@ MX_DEVICE_INLINE int route_id(const RouteParams &p, int64_t i, int64_t end) {
     if (i >= end) return -1;
     const ID v = static_cast<const ID *>(p.ids)[i];
     return v >= 0 && v < (ID)p.groups ? (int)v : -1;
+}
+
+// A lane's ids of kRouteAhead groups of 32, asked for together.
+constexpr int kRouteAhead = 4;
+template <typename ID>
+MX_DEVICE_INLINE void route_ids(const RouteParams &p, int64_t i, int64_t end, int (&id)[kRouteAhead]) {
+#pragma unroll
+    for (int u = 0; u < kRouteAhead; ++u) id[u] = route_id<ID>(p, i + 32 * u, end);
 }
 
 // Exclusive prefix sum of one value per thread over the CTA (warp_sums: 32 ints).
@@ -83,11 +94,17 @@ MX_DEVICE_INLINE void route_count(const RouteParams &p, int64_t begin, int64_t e
     for (int i = threadIdx.x; i < kRouteWarps * p.groups; i += kRouteThreads) cnt[i] = 0;
     __syncthreads();
     const int64_t w0 = begin + warp * per_warp, w1 = min(w0 + per_warp, end);
-    for (int64_t i = w0; i < w1; i += 32) {
-        const int g = route_id<ID>(p, i + lane, w1);
-        const uint32_t same = __match_any_sync(0xffffffffu, g);
-        if (g >= 0 && (__ffs(same) - 1) == lane) cnt[warp * p.groups + g] += __popc(same);
-        __syncwarp();
+    for (int64_t i0 = w0; i0 < w1; i0 += 32 * kRouteAhead) {
+        int id[kRouteAhead];
+        route_ids<ID>(p, i0 + lane, w1, id);
+#pragma unroll
+        for (int u = 0; u < kRouteAhead; ++u) {
+            if (i0 + 32 * u >= w1) break;
+            const int g = id[u];
+            const uint32_t same = __match_any_sync(0xffffffffu, g);
+            if (g >= 0 && (__ffs(same) - 1) == lane) cnt[warp * p.groups + g] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
 }
@@ -97,18 +114,25 @@ template <typename ID>
 MX_DEVICE_INLINE void route_place(const RouteParams &p, int64_t begin, int64_t end, int64_t per_warp, int *cnt) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t w0 = begin + warp * per_warp, w1 = min(w0 + per_warp, end);
-    for (int64_t i = w0; i < w1; i += 32) {
-        const int g = route_id<ID>(p, i + lane, w1);
-        const uint32_t same = __match_any_sync(0xffffffffu, g);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        int at = -1;
-        if (g >= 0) at = cnt[warp * p.groups + g] + rank;
-        __syncwarp();
-        if (g >= 0 && (__ffs(same) - 1) == lane) cnt[warp * p.groups + g] += __popc(same);
-        __syncwarp();
-        if (i + lane < w1) {
-            p.slot[i + lane] = at;
-            if (at >= 0) p.row_token[at] = (int32_t)((i + lane) / p.choices);
+    for (int64_t i0 = w0; i0 < w1; i0 += 32 * kRouteAhead) {
+        int id[kRouteAhead];
+        route_ids<ID>(p, i0 + lane, w1, id);
+#pragma unroll
+        for (int u = 0; u < kRouteAhead; ++u) {
+            const int64_t i = i0 + 32 * u;
+            if (i >= w1) break;
+            const int g = id[u];
+            const uint32_t same = __match_any_sync(0xffffffffu, g);
+            const int rank = __popc(same & ((1u << lane) - 1u));
+            int at = -1;
+            if (g >= 0) at = cnt[warp * p.groups + g] + rank;
+            __syncwarp();
+            if (g >= 0 && (__ffs(same) - 1) == lane) cnt[warp * p.groups + g] += __popc(same);
+            __syncwarp();
+            if (i + lane < w1) {
+                p.slot[i + lane] = at;
+                if (at >= 0) p.row_token[at] = (int32_t)((uint32_t)(i + lane) / (uint32_t)p.choices);   // n < 2^31
+            }
         }
     }
 }
@@ -189,28 +213,51 @@ template <typename ID>
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(RouteParams p) {
     extern __shared__ int cnt[];
     __shared__ int warp_sums[32];
-    __shared__ int first[kRouteMaxGroups];
+    __shared__ int first[kRouteMaxGroups], all[kRouteMaxGroups];
     griddep_launch_dependents();
+    for (int i = threadIdx.x; i < kRouteMaxGroups; i += kRouteThreads) first[i] = all[i] = 0;   // (a barrier in route_count)
     const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, p.n);
     griddep_wait();   // the ids may come from the kernel before the counts
     route_count<ID>(p, begin, end, p.chunk / kRouteWarps, cnt);
-    const int g0 = 2 * threadIdx.x, g1 = g0 + 1;
-    int all0 = 0, all1 = 0, before0 = 0, before1 = 0;
-#pragma unroll 8
-    for (int c = 0; c < p.chunks; ++c) {
-        const int32_t *row = p.counts + (int64_t)c * p.groups;
-        const int c0 = g0 < p.groups ? __ldg(row + g0) : 0, c1 = g1 < p.groups ? __ldg(row + g1) : 0;
-        all0 += c0;
-        all1 += c1;
-        if (c < (int)blockIdx.x) {
-            before0 += c0;
-            before1 += c1;
+    // the counts of all chunks, and of those before this one: the threads share
+    // the experts (two each) and, where that leaves some, the chunks
+    const int width = (p.groups + 1) / 2, slices = kRouteThreads / width, slice = (int)threadIdx.x / width;
+    if (slice < slices) {
+        const int g = 2 * ((int)threadIdx.x - slice * width);
+        const bool two = g + 1 < p.groups;
+        int a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+        for (int c = slice; c < p.chunks; c += 8 * slices) {
+            int v0[8], v1[8];   // eight chunks asked for together
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int cu = c + u * slices;
+                const int32_t *row = p.counts + (int64_t)min(cu, p.chunks - 1) * p.groups + g;
+                v0[u] = __ldg(row);
+                v1[u] = __ldg(row + (two ? 1 : 0));
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int cu = c + u * slices;
+                const bool in = cu < p.chunks, before = cu < (int)blockIdx.x;
+                a0 += in ? v0[u] : 0;
+                a1 += in ? v1[u] : 0;
+                b0 += before ? v0[u] : 0;
+                b1 += before ? v1[u] : 0;
+            }
+        }
+        atomicAdd(&all[g], a0);
+        atomicAdd(&first[g], b0);
+        if (two) {
+            atomicAdd(&all[g + 1], a1);
+            atomicAdd(&first[g + 1], b1);
         }
     }
+    __syncthreads();
+    const int g0 = 2 * threadIdx.x, g1 = g0 + 1;
     int o0, o1;
-    const int total = route_offsets(p, all0, all1, warp_sums, o0, o1);
-    if (g0 < p.groups) first[g0] = o0 + before0;
-    if (g1 < p.groups) first[g1] = o1 + before1;
+    const int total = route_offsets(p, g0 < p.groups ? all[g0] : 0, g1 < p.groups ? all[g1] : 0, warp_sums, o0, o1);
+    if (g0 < p.groups) first[g0] += o0;
+    if (g1 < p.groups) first[g1] += o1;
     if (blockIdx.x == 0) {
         if (g0 < p.groups) p.offsets[g0] = o0;
         if (g1 < p.groups) p.offsets[g1] = o1;
@@ -236,6 +283,8 @@ struct CombineParams {
 };
 
 // One thread: VEC columns of one token, the choices eight loads at a time.
+// Bound by HBM: 16384 tokens x 8 choices (a twentieth dropped) x 4096 180 us,
+// 6.4 TB/s; 32 x 8 2.3 us.
 template <int VEC>
 __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
     const int64_t t = blockIdx.x;
