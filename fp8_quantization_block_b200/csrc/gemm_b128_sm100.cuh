@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
         if (warp == 0 && !p.skip_producer) {
             // -------------------------------------------------------- producer
             B128Tiles<GROUPED> tiles(p, lane);
+            const bool elected = elect_one();
             int used = 0, s = 0;
             uint32_t ph = 0;
             bool stop = false;
@@ -246,12 +247,12 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                 // GROUPED: of A only the 32-row boxes that hold rows of the group
                 const int boxes = GROUPED ? min(p.a_bytes / (32 * kStageKBytes), (t.row_end - t.row0 + 31) / 32) : 0;
                 const uint32_t tx = (uint32_t)((GROUPED ? boxes * 32 * kStageKBytes : p.a_bytes) + p.b_bytes);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!mbar_wait_at(empty0 + 8u * (uint32_t)s, ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
-                        stop = true;
-                        break;
-                    }
-                    if (lane == 0) {
+                if (elected)
+                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                        if (!mbar_wait_at(empty0 + 8u * (uint32_t)s, ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
+                            stop = true;
+                            break;
+                        }
                         mbar_arrive_expect_tx(&full[s], tx);
                         if (GROUPED)
                             for (int b = 0; b < boxes; ++b)
@@ -260,14 +261,13 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                         else
                             tma_load_2d(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, t.row0, &full[s]);
                         tma_load_2d(smem_b + s * p.b_bytes, &tmB, kb * kStageKBytes, b_row, &full[s]);
+                        ++used;
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
-                    __syncwarp();
-                    ++used;
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
+                stop = __any_sync(0xffffffffu, stop);
             }
             // copies in flight land before this CTA may leave
             for (int u = max(0, used - S); u < used; ++u)
@@ -278,41 +278,46 @@ __global__ void __launch_bounds__(kB128Threads, 1)
             const uint64_t ad0 = desc | (uint64_t)((smem_u32(smem_a) >> 4) & 0x3FFFu);
             const uint64_t bd0 = desc | (uint64_t)((smem_u32(smem_b) >> 4) & 0x3FFFu);
             const uint32_t idesc = b128_idesc(p.bn);
-            const uint32_t leader = lane == 0 ? 1u : 0u;
+            const bool leader = elect_one();
             B128Tiles<GROUPED> tiles(p, lane);
             int s = 0, pi = 0;
             uint32_t ph = 0, pph = 0;
-            bool stop = false, full_ok = false, empty_ok = false;   // the next block's barriers, as asked ahead
+            bool stop = false;
             B128Tile t;
             for (int i = worker; !stop && tiles.at(i, t); i += workers) {
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if ((!full_ok && !mbar_wait_at(full0 + 8u * (uint32_t)s, ph, p.wait_limit_ns, SITE_GEMM_MMA_FULL, abort_flag)) ||
-                        (!empty_ok &&
-                         !mbar_wait_at(pempty0 + 8u * (uint32_t)pi, pph ^ 1u, p.wait_limit_ns, SITE_GEMM_MMA_ACC_EMPTY, abort_flag))) {
-                        stop = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = ad0 + (uint64_t)(s * (p.a_bytes >> 4)), bd = bd0 + (uint64_t)(s * (p.b_bytes >> 4));
-                    const uint32_t d = tmem + (uint32_t)(pi * kPartialCols);
+                // One elected thread runs the blocks (here and in the producer):
+                // a tcgen05 instruction then issues in some 20 cycles; predicated
+                // by lane, or under lane == 0, in 64 and more.  Tiles of few
+                // columns were bound by that: 16 x 8192 x 8192 25.5 -> 21.0 us,
+                // 16 x 4096 x 4096 14.4 -> 11.3.
+                if (leader)
+                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                        if (!mbar_wait_at(full0 + 8u * (uint32_t)s, ph, p.wait_limit_ns, SITE_GEMM_MMA_FULL, abort_flag) ||
+                            !mbar_wait_at(pempty0 + 8u * (uint32_t)pi, pph ^ 1u, p.wait_limit_ns, SITE_GEMM_MMA_ACC_EMPTY,
+                                          abort_flag)) {
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = ad0 + (uint64_t)(s * (p.a_bytes >> 4)), bd = bd0 + (uint64_t)(s * (p.b_bytes >> 4));
+                        const uint32_t d = tmem + (uint32_t)(pi * kPartialCols);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        tc_mma_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, leader);
-                    tc_commit_if(&pfull[pi], leader);
-                    tc_commit_if(&empty[s], leader);
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
+                        for (int j = 0; j < 4; ++j)
+                            tc_mma_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, 1u);
+                        tc_commit_if(&pfull[pi], 1u);
+                        tc_commit_if(&empty[s], 1u);
+                        if (++s == S) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                        if (++pi == NP) {
+                            pi = 0;
+                            pph ^= 1u;
+                        }
                     }
-                    if (++pi == NP) {
-                        pi = 0;
-                        pph ^= 1u;
-                    }
-                    full_ok = mbar_test_at(full0 + 8u * (uint32_t)s, ph);
-                    empty_ok = mbar_test_at(pempty0 + 8u * (uint32_t)pi, pph ^ 1u);
-                }
+                stop = __any_sync(0xffffffffu, stop);
             }
-            tc_commit_if(mma_done, leader);
+            if (leader) tc_commit_if(mma_done, 1u);
             __syncwarp();
         } else if (warp >= 2) {
             // -------------------------------------------------------- scales

@@ -164,6 +164,13 @@ MX_DEVICE_INLINE bool mbar_test_at(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// One thread of the (whole) warp, the same at every call: tcgen05.commit tracks the
+// issuing thread's own instructions.
+MX_DEVICE_INLINE bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
 // Arrive by the threads whose `on` flag is set, without a branch.
 MX_DEVICE_INLINE void mbar_arrive_at_if(uint32_t bar, uint32_t on) {
     asm volatile("{\n\t.reg .b64 st;\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"

@@ -28,14 +28,16 @@ cudaLaunchConfig_t launch_cfg(dim3 grid, int threads, size_t smem, cudaStream_t 
 // --- tiles of the block-128 GEMM ------------------------------------------------
 // Columns of a tile: those of the shortest run, waves of tiles times the cycles
 // of a tile's K block.  The drain sets these: with two chunks per warp (up to
-// 128 columns) about 740 + 0.2 bn, with four 900 + 0.6 bn (16 x 8192 x 8192, one
-// wave either way: 64 to 128 columns 25.3 us, 160 to 224 33 to 34, 256 35.8;
-// 16 x 28672 x 8192: 128 columns in two waves 49.9 us, 224 in one 40.7).
+// 128 columns) about 600 + 0.1 bn, with four 900 + 0.85 bn (128 x 8192 x 8192,
+// one wave either way: 64 to 128 columns 22.4 us, 160 35.8, 256 38.7; 16 x 28672
+// x 8192: 128 columns in two waves 46.2 us, 224 in one 41.2; 4096^3: 128 in
+// seven waves 78.1, 256 in four 82.8; 2048 x 2048 x 4096: 128 in two 24.3, 256 in
+// one 23.2).
 int b128_columns(int64_t n, int64_t row_blocks, int sms) {
     int best = 256;
     double best_cost = 1e300;
     for (int bn = 256; bn >= 32; bn -= 32) {
-        const double cost = (double)cdiv(row_blocks * cdiv(n, bn), sms) * (bn <= 128 ? 740.0 + 0.2 * bn : 900.0 + 0.6 * bn);
+        const double cost = (double)cdiv(row_blocks * cdiv(n, bn), sms) * (bn <= 128 ? 600.0 + 0.1 * bn : 900.0 + 0.85 * bn);
         if (cost < best_cost) {
             best_cost = cost;
             best = bn;
