@@ -837,7 +837,8 @@ NCU_TRAFFIC = {
                   "src": "db2404893c911f15"},
 }
 # csrc files that no GEMM of gemm_sm100.cuh / gemm_pair_sm100.cuh includes
-OTHER_KERNELS = ("gemm_mbs_sm100.cuh", "rotate.cuh")
+OTHER_KERNELS = ("gemm_mbs_sm100.cuh", "rotate.cuh", "gemm_b128_sm100.cuh", "gemm_grouped_sm100.cuh", "groups.cuh",
+                 "mx_experts.cu", "quantize_b128.cuh", "routing.cuh")
 
 
 def csrc_hash(exclude=OTHER_KERNELS) -> str:

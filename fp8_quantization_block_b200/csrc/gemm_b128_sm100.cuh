@@ -34,6 +34,13 @@
 // weight stream, spread over all SMs.  (256-row tiles on pairs of CTAs, with a
 // third less L2 traffic, took the same time at every size from 512 x 4096 x
 // 4096 to 8192^3: the drain sets the pace, not the loads.)
+//
+// Bound by the weights' stream at few rows (16 x 28672 x 8192 41 us, 5.8 TB/s;
+// narrower matrices, with a block's fixed 0.3 us on each CTA, do not reach it:
+// 16 x 8192 x 8192 22 us, 3.0 TB/s), by the drain and the SMs' intake from L2 at
+// many (a 256-column block takes some 1100 cycles where its MMAs take 512:
+// 4096^3 79 us, 8192^3 560 us alone and 615 to 690 in a loop at the power limit,
+// 1.6 to 1.9 PFLOP/s).
 #pragma once
 
 #include "gemm_sm100.cuh"

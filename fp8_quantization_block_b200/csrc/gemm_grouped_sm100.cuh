@@ -9,6 +9,11 @@
 // rows past the group's end are the next group's or past the matrix, and only
 // produce accumulator rows that are not stored.  Tiles of a group run rows
 // fastest: neighbouring CTAs share a 256-row slice of B_g.
+//
+// Bound by the weights' stream where groups are small (64 groups of 8 rows, 4096
+// x 2048: MXFP8 92 us, 6.0 TB/s; NVFP4 52 us, 5.8 TB/s), and by what an SM takes
+// in from L2, 54 KB per 128-byte stage at some 55 B per clock, where they are
+// larger (32 groups of 125 rows on average, 4096 x 4096: MXFP8 127 us, NVFP4 71).
 #pragma once
 
 #include "gemm_sm100.cuh"
@@ -151,7 +156,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint64_t desc_ab = smem_desc(0, 16, 1024, 2);
         const uint64_t ad0 = desc_ab | (uint64_t)((smem_u32(smem + L::kOffA) >> 4) & 0x3FFFu);
         const uint64_t bd0 = desc_ab | (uint64_t)((smem_u32(smem + L::kOffB) >> 4) & 0x3FFFu);
-        const uint32_t leader = lane == 0 ? 1u : 0u;
+        const bool elected = elect_one();
+        const uint32_t leader = elected ? 1u : 0u;
         const uint32_t ab = FMT == kGemmRuntimeTypes ? p.ab_types : 0u;
         int last_n_mma, last_n_chunk;
         stage_extent<FMT>(p.num_kt - 1, p.K, last_n_mma, last_n_chunk);
@@ -162,10 +168,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t t_acc = tmem + (uint32_t)((it & 1) * L::kAccStride);
             auto run_stage = [&](int k, uint32_t acc) {
                 const uint32_t t_sfa = tmem + (uint32_t)(L::kTmemSf + slot * L::kSfSlotCols);
-                issue_stage<FMT, false, BN, 4 * L::kBBands>(
-                    k + 1 < p.num_kt ? 4 : last_n_mma, t_acc, ad0 + (uint64_t)(s * (L::kABytes >> 4)),
-                    bd0 + (uint64_t)(s * (L::kBBytes >> 4)), t_sfa, t_sfa + 4 * F::kChunks, acc, leader, ab);
-                tc_commit_if(&empty[s], leader);
+                // by one elected thread: 2 to 3% of the FP4 products against a
+                // predicate over the warp (64 groups of 8 rows, 4096 x 2048
+                // NVFP4: 53.1 -> 51.6 us)
+                if (elected) {
+                    issue_stage<FMT, false, BN, 4 * L::kBBands>(
+                        k + 1 < p.num_kt ? 4 : last_n_mma, t_acc, ad0 + (uint64_t)(s * (L::kABytes >> 4)),
+                        bd0 + (uint64_t)(s * (L::kBBytes >> 4)), t_sfa, t_sfa + 4 * F::kChunks, acc, 1u, ab);
+                    tc_commit_if(&empty[s], 1u);
+                }
+                __syncwarp();
                 s = (s + 1 == STAGES) ? 0 : s + 1;
                 slot = (slot + 1 == L::kSlots) ? 0 : slot + 1;
                 ++kg;
