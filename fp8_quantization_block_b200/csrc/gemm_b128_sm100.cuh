@@ -12,11 +12,12 @@
 // the running sums, which stay in registers (FP32) for the whole tile.
 //
 // Persistent kernel, 12 warps:
-//   warp 0       TMA producer of A and B (128 bytes of K = one block per
-//                stage, 128-byte swizzle) into a ring that runs on across tiles;
-//   warp 1       TMEM owner and MMA issuer: 4 MMAs of K = 32 per stage into one
-//                of the partial buffers (2 of 256 columns, or 4 of 128), which
-//                then holds that block's P_b alone;
+//   warp 0       TMA producer of A and B (blocks of 128 bytes of K, 128-byte
+//                swizzle, one to four per stage) into a ring that runs on across
+//                tiles;
+//   warp 1       TMEM owner and MMA issuer: 4 MMAs of K = 32 per block into one
+//                of the partial buffers (2 of 256 columns, 4 of 128 or 8 of 64),
+//                which then holds that block's P_b alone;
 //   warps 2-3    scales: the rows' sA and the tile's (at most three) sB of each
 //                block, copied asynchronously into a ring in shared memory up to
 //                16 blocks ahead (their latency beside a saturated weight
@@ -36,10 +37,10 @@
 // 4096 to 8192^3: the drain sets the pace, not the loads.)
 //
 // Bound by the weights' stream at few rows (16 x 28672 x 8192 41 us, 5.8 TB/s;
-// narrower matrices, with a block's fixed 0.3 us on each CTA, do not reach it:
-// 16 x 8192 x 8192 22 us, 3.0 TB/s), by the drain and the SMs' intake from L2 at
+// narrower matrices, with at least 0.15 us per block on each CTA, do not reach it:
+// 16 x 8192 x 8192 15.5 us, 4.3 TB/s), by the drain and the SMs' intake from L2 at
 // many (a 256-column block takes some 1100 cycles where its MMAs take 512:
-// 4096^3 79 us, 8192^3 560 us alone and 615 to 690 in a loop at the power limit,
+// 4096^3 77 us, 8192^3 560 us alone and 615 to 690 in a loop at the power limit,
 // 1.6 to 1.9 PFLOP/s).
 #pragma once
 
@@ -179,21 +180,25 @@ MX_DEVICE_INLINE uint32_t bf16_pair(float a, float b) {
 }
 
 // CH: 32-column chunks per drain warp (4: tiles of up to 256 columns and two
-// partial buffers; 2: up to 128 columns and four partial buffers).
+// partial buffers; 2: up to 128 columns and four; 1: up to 64 and eight).
 // VIA_TMEM: results are stored through TMEM (GELU, rows of C off 16 bytes); a
 // variant of its own, since that path in the same code costs the loop before it
 // registers (8192^3: 1200 against 1090 cycles per block).
-template <int CH, bool GROUPED, bool VIA_TMEM>
+// PB: K blocks per stage of the ring and per unit of partial buffers, which share
+// one round of barriers (a last unit's missing blocks are brought as zeros and
+// scaled by a neighbour's scales).  16 x 8192 x 8192 with one, two and four blocks
+// 22.1, 16.6 and 15.5 us, the first in 128 columns' code (64 columns, CH = 2).
+template <int CH, int PB, bool GROUPED, bool VIA_TMEM>
 __global__ void __launch_bounds__(kB128Threads, 1)
     gemm_b128_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const B128GemmParams p) {
     constexpr int kPartialCols = CH * 64;
-    constexpr int NP = 512 / kPartialCols;
+    constexpr int NP = 512 / (kPartialCols * PB);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int S = p.stages;
-    uint8_t *smem_a = smem, *smem_b = smem + S * p.a_bytes;
-    float *scale_ring = reinterpret_cast<float *>(smem_b + S * p.b_bytes);   // [slots][kB128SlotFloats]
+    uint8_t *smem_a = smem, *smem_b = smem + S * PB * p.a_bytes;
+    float *scale_ring = reinterpret_cast<float *>(smem_b + S * PB * p.b_bytes);   // [slots][kB128SlotFloats]
     uint8_t *staging = reinterpret_cast<uint8_t *>(scale_ring + kB128ScaleSlots * kB128SlotFloats);
     uint64_t *full = reinterpret_cast<uint64_t *>(staging + p.staging_bytes);
     uint64_t *empty = full + kB128MaxStages;
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
     griddep_wait();
 
     if (warp < 4) {
-        if (CH == 4) setmaxnreg_dec<kB128OtherRegs>();
+        setmaxnreg_dec<kB128OtherRegs>();
         if (warp == 0 && !p.skip_producer) {
             // -------------------------------------------------------- producer
             B128Tiles<GROUPED> tiles(p, lane);
@@ -253,21 +258,25 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                 const int b_row = t.group * p.N + t.n0;
                 // GROUPED: of A only the 32-row boxes that hold rows of the group
                 const int boxes = GROUPED ? min(p.a_bytes / (32 * kStageKBytes), (t.row_end - t.row0 + 31) / 32) : 0;
-                const uint32_t tx = (uint32_t)((GROUPED ? boxes * 32 * kStageKBytes : p.a_bytes) + p.b_bytes);
+                const uint32_t tx = (uint32_t)(PB * ((GROUPED ? boxes * 32 * kStageKBytes : p.a_bytes) + p.b_bytes));
                 if (elected)
-                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                    for (int kb = 0; kb < p.num_kb; kb += PB) {
                         if (!mbar_wait_at(empty0 + 8u * (uint32_t)s, ph ^ 1u, p.wait_limit_ns, SITE_GEMM_PRODUCER_EMPTY, abort_flag)) {
                             stop = true;
                             break;
                         }
                         mbar_arrive_expect_tx(&full[s], tx);
-                        if (GROUPED)
-                            for (int b = 0; b < boxes; ++b)
-                                tma_load_2d(smem_a + s * p.a_bytes + b * 32 * kStageKBytes, &tmA, kb * kStageKBytes,
-                                            t.row0 + 32 * b, &full[s]);
-                        else
-                            tma_load_2d(smem_a + s * p.a_bytes, &tmA, kb * kStageKBytes, t.row0, &full[s]);
-                        tma_load_2d(smem_b + s * p.b_bytes, &tmB, kb * kStageKBytes, b_row, &full[s]);
+#pragma unroll
+                        for (int j = 0; j < PB; ++j) {   // (a block past the last is brought as zeros)
+                            uint8_t *a = smem_a + (s * PB + j) * p.a_bytes;
+                            const int k0 = (kb + j) * kStageKBytes;
+                            if (GROUPED)
+                                for (int b = 0; b < boxes; ++b)
+                                    tma_load_2d(a + b * 32 * kStageKBytes, &tmA, k0, t.row0 + 32 * b, &full[s]);
+                            else
+                                tma_load_2d(a, &tmA, k0, t.row0, &full[s]);
+                            tma_load_2d(smem_b + (s * PB + j) * p.b_bytes, &tmB, k0, b_row, &full[s]);
+                        }
                         ++used;
                         if (++s == S) {
                             s = 0;
@@ -295,10 +304,10 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                 // One elected thread runs the blocks (here and in the producer):
                 // a tcgen05 instruction then issues in some 20 cycles; predicated
                 // by lane, or under lane == 0, in 64 and more.  Tiles of few
-                // columns were bound by that: 16 x 8192 x 8192 25.5 -> 21.0 us,
-                // 16 x 4096 x 4096 14.4 -> 11.3.
+                // columns were bound by that: 16 x 8192 x 8192 25.5 us so, 22.1
+                // elected (one block per stage).
                 if (leader)
-                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                    for (int kb = 0; kb < p.num_kb; kb += PB) {
                         if (!mbar_wait_at(full0 + 8u * (uint32_t)s, ph, p.wait_limit_ns, SITE_GEMM_MMA_FULL, abort_flag) ||
                             !mbar_wait_at(pempty0 + 8u * (uint32_t)pi, pph ^ 1u, p.wait_limit_ns, SITE_GEMM_MMA_ACC_EMPTY,
                                           abort_flag)) {
@@ -306,11 +315,15 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t ad = ad0 + (uint64_t)(s * (p.a_bytes >> 4)), bd = bd0 + (uint64_t)(s * (p.b_bytes >> 4));
-                        const uint32_t d = tmem + (uint32_t)(pi * kPartialCols);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            tc_mma_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, 1u);
+                        for (int b = 0; b < PB; ++b) {
+                            const uint64_t ad = ad0 + (uint64_t)((s * PB + b) * (p.a_bytes >> 4));
+                            const uint64_t bd = bd0 + (uint64_t)((s * PB + b) * (p.b_bytes >> 4));
+                            const uint32_t d = tmem + (uint32_t)((pi * PB + b) * kPartialCols);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tc_mma_f8_if(d, ad + 2u * j, bd + 2u * j, idesc, j > 0 ? 1u : 0u, 1u);
+                        }
                         tc_commit_if(&pfull[pi], 1u);
                         tc_commit_if(&empty[s], 1u);
                         if (++s == S) {
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
         }
     } else {
         // ------------------------------------------------------------ drain
-        if (CH == 4) setmaxnreg_inc<kB128DrainRegs>();
+        setmaxnreg_inc<kB128DrainRegs>();
         const int q = warp & 3;                       // TMEM lane quadrant
         const int half = (warp - 4) >> 2;
         // this warp's chunks: CH of them whatever bn is (the loop below has to be
@@ -411,17 +424,27 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     break;
                 }
                 uint32_t f = ring + g * (uint32_t)(kB128ScaleGroup * kB128SlotFloats * 4);
-                float fa = ld_shared_f32(f + my_row), fb0 = ld_shared_f32(f + my_col);
-                float fb1 = ld_shared_f32(f + my_col + 4);   // (a fourth column block is never used)
                 const int kb1 = min(kb0 + kB128ScaleGroup, p.num_kb);
+                // the scales of PB blocks from f (the last ones again past the end)
+                float fa[PB], fb0[PB], fb1[PB];
+                auto scales = [&](int kb) {
+#pragma unroll
+                    for (int b = 0; b < PB; ++b) {
+                        const uint32_t at = f + (b > 0 && kb + b < kb1 ? (uint32_t)(b * kB128SlotFloats * 4) : 0u);
+                        fa[b] = ld_shared_f32(at + my_row);
+                        fb0[b] = ld_shared_f32(at + my_col);
+                        fb1[b] = ld_shared_f32(at + my_col + 4);   // (a fourth column block is never used)
+                    }
+                };
+                scales(kb0);
 #pragma unroll 1
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = kb0; kb < kb1; kb += PB) {
                     if (!ready && !mbar_wait_at(pfull0 + 8u * pi, pph, p.wait_limit_ns, SITE_GEMM_EPI_ACC, abort_flag)) {
                         stop = true;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t cur = pi, t_p = t_lane + pi * (uint32_t)kPartialCols;
+                    const uint32_t cur = pi, t_p = t_lane + pi * (uint32_t)(PB * kPartialCols);
                     if (++pi == NP) {
                         pi = 0;
                         pph ^= 1u;
@@ -429,29 +452,33 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                     if (any) {
                         // Straight code, nothing conditional: a chunk's load runs
                         // while the one before it is folded in, and the next
-                        // block's scales and barrier are asked for on the way.
-                        // (The drain alone, on one SM: 565 cycles per block with a
-                        // test per chunk, 517 as a plain sequence, 476 like this,
-                        // of the 512 that the block's MMAs take.)
+                        // blocks' scales and barrier are asked for on the way.
+                        // (The drain alone, on one SM, CH = 4: 565 cycles per block
+                        // with a test per chunk, 517 as a plain sequence, 476 like
+                        // this, of the 512 that the block's MMAs take.)
                         uint32_t r[2][32];
                         tmem_ld32(t_p, r[0]);
-                        const float f0 = fa * fb0, f1 = fa * fb1;
-                        const uint64_t F0 = pk2(f0, f0), F1 = pk2(f1, f1);
-                        f += kb + 1 < kb1 ? (uint32_t)(kB128SlotFloats * 4) : 0u;
-                        fa = ld_shared_f32(f + my_row);
-                        fb0 = ld_shared_f32(f + my_col);
-                        fb1 = ld_shared_f32(f + my_col + 4);
+                        uint64_t F0[PB], F1[PB];
 #pragma unroll
-                        for (int h = 0; h < CH; ++h) {
+                        for (int b = 0; b < PB; ++b) {
+                            const float f0 = fa[b] * fb0[b], f1 = fa[b] * fb1[b];
+                            F0[b] = pk2(f0, f0);
+                            F1[b] = pk2(f1, f1);
+                        }
+                        f += kb + PB < kb1 ? (uint32_t)(PB * kB128SlotFloats * 4) : 0u;
+                        scales(kb + PB);
+#pragma unroll
+                        for (int i = 0; i < PB * CH; ++i) {
+                            const int h = i % CH;
                             tmem_wait_ld();
-                            if (h + 1 < CH) tmem_ld32(t_p + 32 * (h + 1), r[(h + 1) & 1]);
-                            else release(cur, !VIA_TMEM || kb + 1 < p.num_kb ? 1u : 0u);
-                            if (h == (CH > 1 ? CH - 2 : 0)) ready = mbar_test_at(pfull0 + 8u * pi, pph);
-                            const uint64_t F = h < split ? F0 : F1;
+                            if (i + 1 < PB * CH) tmem_ld32(t_p + (i + 1) / CH * kPartialCols + 32 * ((i + 1) % CH), r[(i + 1) & 1]);
+                            else release(cur, !VIA_TMEM || kb + PB < p.num_kb ? 1u : 0u);
+                            if (i == PB * CH - 2) ready = mbar_test_at(pfull0 + 8u * pi, pph);
+                            const uint64_t F = h < split ? F0[i / CH] : F1[i / CH];
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
-                                acc[16 * h + c] = fma2(pk2(__uint_as_float(r[h & 1][2 * c]),
-                                                           __uint_as_float(r[h & 1][2 * c + 1])), F, acc[16 * h + c]);
+                                acc[16 * h + c] = fma2(pk2(__uint_as_float(r[i & 1][2 * c]),
+                                                           __uint_as_float(r[i & 1][2 * c + 1])), F, acc[16 * h + c]);
                         }
                     } else {
                         release(cur, 1u);
@@ -492,7 +519,7 @@ __global__ void __launch_bounds__(kB128Threads, 1)
                 // The sums go back to TMEM, so that one short loop can index
                 // them: unrolled over 128 registers, GELU's code outgrows the
                 // instruction cache.
-                const uint32_t t_p = t_lane + last * (uint32_t)kPartialCols;
+                const uint32_t t_p = t_lane + last * (uint32_t)(PB * kPartialCols);
 #pragma unroll
                 for (int c = 0; c < CH * 2; ++c) {
                     uint32_t r[16];

@@ -27,17 +27,17 @@ cudaLaunchConfig_t launch_cfg(dim3 grid, int threads, size_t smem, cudaStream_t 
 
 // --- tiles of the block-128 GEMM ------------------------------------------------
 // Columns of a tile: those of the shortest run, waves of tiles times the cycles
-// of a tile's K block.  The drain sets these: with two chunks per warp (up to
-// 128 columns) about 600 + 0.1 bn, with four 900 + 0.85 bn (128 x 8192 x 8192,
-// one wave either way: 64 to 128 columns 22.4 us, 160 35.8, 256 38.7; 16 x 28672
-// x 8192: 128 columns in two waves 46.2 us, 224 in one 41.2; 4096^3: 128 in
-// seven waves 78.1, 256 in four 82.8; 2048 x 2048 x 4096: 128 in two 24.3, 256 in
-// one 23.2).
+// of a tile's K block.  The drain sets these: with one chunk per warp (up to 64
+// columns) about 440 + 0.1 bn, with two (128) 600 + 0.1 bn, with four 900 +
+// 0.85 bn (128 x 8192 x 8192, one wave each: 64 columns 17.6 us, 128 20.5, 160
+// 35.8, 256 38.7; 16 x 28672 x 8192: 128 columns in two waves 46.2 us, 224 in one
+// 41.2; 4096^3: 128 in seven waves 75.9, 256 in four 82.8; 2048 x 2048 x 4096: 128
+// in two 24.3, 256 in one 23.2).
 int b128_columns(int64_t n, int64_t row_blocks, int sms) {
     int best = 256;
     double best_cost = 1e300;
     for (int bn = 256; bn >= 32; bn -= 32) {
-        const double cost = (double)cdiv(row_blocks * cdiv(n, bn), sms) * (bn <= 128 ? 600.0 + 0.1 * bn : 900.0 + 0.85 * bn);
+        const double cost = (double)cdiv(row_blocks * cdiv(n, bn), sms) * ((bn <= 64 ? 440.0 : bn <= 128 ? 600.0 : 900.0) + (bn <= 128 ? 0.1 : 0.85) * bn);
         if (cost < best_cost) {
             best_cost = cost;
             best = bn;
@@ -46,10 +46,10 @@ int b128_columns(int64_t n, int64_t row_blocks, int sms) {
     return best;
 }
 
-template <int CH, bool GROUPED, bool VIA>
+template <int CH, int PB, bool GROUPED, bool VIA>
 mx_status launch_b128_t(const CUtensorMap &ta, const CUtensorMap &tb, const B128GemmParams &p, int workers, size_t smem,
                         cudaStream_t st) {
-    const auto kern = gemm_b128_kernel<CH, GROUPED, VIA>;
+    const auto kern = gemm_b128_kernel<CH, PB, GROUPED, VIA>;
     if (smem_limit_once(reinterpret_cast<const void *>(kern), kSmemLimit) != cudaSuccess) return MX_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = launch_cfg(dim3((unsigned)workers, 1, 1), kB128Threads, smem, st, attr);
@@ -78,9 +78,17 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     p.vec_store = ldc % 16 == 0 && base % 32 == 0 ? 2 : (ldc % 8 == 0 && base % 16 == 0 ? 1 : 0);
     p.staging_bytes = p.vec_store ? 0 : kB128StagingBytes;
     const int fixed = kB128FixedBytes + p.staging_bytes;
-    p.stages = (kSmemLimit - fixed) / (p.a_bytes + p.b_bytes);
+    // K blocks per stage: one where a warp has four chunks, else as many as leave
+    // three stages or more (64 columns, 8192 x 8192: 128 rows with two 17.6 us, with
+    // four, in two stages, 20.7; 32 rows with four 15.5, with two 16.6); one where
+    // two chunks' results go through TMEM, whose code leaves no registers for the
+    // second block (1000 x 2179 x 1152 10.3 us, with two 10.7).
+    const bool via = epilogue == MX_EPI_GELU || p.vec_store == 0;
+    const int blocks = p.bn > 128 || (p.bn > 64 && via) ? 1 : p.bn > 64 || groups || p.bm_shift > 5 ? 2 : 4;
+    const int stage = blocks * (p.a_bytes + p.b_bytes);
+    p.stages = (kSmemLimit - fixed) / stage;
     if (p.stages > kB128MaxStages) p.stages = kB128MaxStages;
-    const size_t smem = (size_t)fixed + (size_t)p.stages * (p.a_bytes + p.b_bytes);
+    const size_t smem = (size_t)fixed + (size_t)p.stages * stage;
     CUtensorMap ta, tb;
     if (!make_tmap_u8(&ta, A->codes, M, K, groups ? 32 : 1 << p.bm_shift)) return MX_ERR_CUDA;
     if (!make_tmap_u8(&tb, B->codes, G * N, K, p.bn)) return MX_ERR_CUDA;
@@ -103,14 +111,19 @@ mx_status launch_gemm_b128(const mx_tensor *A, const mx_tensor *B, const mx_grou
     if (tiles > INT32_MAX) return MX_ERR_UNSUPPORTED_SHAPE;
     int workers = cap > 0 && cap < sms ? cap : sms;
     if (workers > tiles) workers = (int)tiles;
-    const bool via = epilogue == MX_EPI_GELU || p.vec_store == 0;
-#define MX_LAUNCH(CH)                                                                     \
-    return groups ? (via ? launch_b128_t<CH, true, true>(ta, tb, p, workers, smem, st)    \
-                         : launch_b128_t<CH, true, false>(ta, tb, p, workers, smem, st))  \
-                  : (via ? launch_b128_t<CH, false, true>(ta, tb, p, workers, smem, st)   \
-                         : launch_b128_t<CH, false, false>(ta, tb, p, workers, smem, st))
-    if (p.bn > 128) MX_LAUNCH(4);
-    MX_LAUNCH(2);
+#define MX_LAUNCH(CH, PB, VIA)                                                  \
+    return groups ? launch_b128_t<CH, PB, true, VIA>(ta, tb, p, workers, smem, st) \
+                  : launch_b128_t<CH, PB, false, VIA>(ta, tb, p, workers, smem, st)
+    if (via) {
+        if (p.bn > 128) MX_LAUNCH(4, 1, true);
+        if (p.bn > 64) MX_LAUNCH(2, 1, true);
+        if (blocks == 2) MX_LAUNCH(1, 2, true);
+        return launch_b128_t<1, 4, false, true>(ta, tb, p, workers, smem, st);
+    }
+    if (p.bn > 128) MX_LAUNCH(4, 1, false);
+    if (p.bn > 64) MX_LAUNCH(2, 2, false);
+    if (blocks == 2) MX_LAUNCH(1, 2, false);
+    return launch_b128_t<1, 4, false, false>(ta, tb, p, workers, smem, st);
 #undef MX_LAUNCH
 }
 

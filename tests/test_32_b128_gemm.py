@@ -151,3 +151,17 @@ def test_fused_call_without_allocation_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kb", [1, 2, 3, 4, 5, 6, 7, 9])
+@pytest.mark.parametrize("M,N", [(5, 700), (32, 64), (33, 1000), (128, 4096), (300, 5000), (40, 333)])
+def test_any_number_of_blocks(M, N, kb):
+    """Stages of one, two and four K blocks with every remainder; several tiles per CTA, whose rings run on."""
+    try:
+        mx.check(mx.mx_debug_set(mx.MX_DEBUG_MAX_GEMM_CTAS, 3))
+        _, _, c = run(M, N, 128 * kb)
+    finally:
+        mx.mx_debug_set(mx.MX_DEBUG_MAX_GEMM_CTAS, 0)
+    a, b = mx.quantize(activations(M, M, 128 * kb), 6), mx.quantize(weights(N, N, 128 * kb), 8)
+    g = mx.gemm_fused_act(activations(M, M, 128 * kb), b, epilogue=mx.MX_EPI_GELU)
+    assert gemm_error(g, b128_values(a), b128_values(b), True) <= 1.0
