@@ -33,7 +33,7 @@ def test_sizes():
     assert mx.mx_grouped_scales_bytes(0, 3, 100, 256) == 3 * 128 * 8               # at most a band per row
     assert mx.mx_grouped_scales_bytes(8, 3, 1, 256) == 0 and mx.mx_grouped_scales_bytes(5, 3, 1, 256) == 0
     assert mx.mx_route_workspace_bytes(256, 8, 64) == 0
-    assert mx.mx_route_workspace_bytes(257, 8, 64) == 2 * 64 * 4
+    assert mx.mx_route_workspace_bytes(257, 8, 64) == 3 * 64 * 4                    # counts of three chunks of 1024
     assert mx.mx_route_workspace_bytes(2 ** 31, 2, 4) == 0
     assert ctypes.sizeof(mx.MxGroupsC) == 16
     assert mx.MX_MAX_GROUPS == 1024
