@@ -361,7 +361,7 @@ def dequantize(t: MxTensor, out: torch.Tensor | None = None, stream=None) -> tor
     if (ctx := _elsewhere(t.codes)) is not None:
         with ctx:
             return dequantize(t, out, stream)
-    out = out if out is not None else torch.empty((t.rows, t.cols), dtype=torch.bfloat16, device=t.codes.device)
+    out = out if out is not None else torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.codes.device)
     check(mx_dequantize(t.c(), out.data_ptr(), out.stride(0), _stream(stream)), "mx_dequantize")
     return out
 
@@ -370,7 +370,7 @@ def gemm(A: MxTensor, B: MxTensor, out: torch.Tensor | None = None, stream=None)
     if (ctx := _elsewhere(A.codes)) is not None:
         with ctx:
             return gemm(A, B, out, stream)
-    out = out if out is not None else torch.empty((A.rows, B.rows), dtype=torch.bfloat16, device=A.codes.device)
+    out = out if out is not None else torch.empty(A.rows, B.rows, dtype=torch.bfloat16, device=A.codes.device)
     check(mx_gemm(A.c(), B.c(), out.data_ptr(), out.stride(0), _stream(stream)), "mx_gemm")
     return out
 
@@ -392,7 +392,7 @@ def gemm_fused_act(x: torch.Tensor, W: MxTensor, out: torch.Tensor | None = None
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     M, K = x.shape
     fmt = _act_fmt(W) if x_fmt is None else x_fmt
-    out = out if out is not None else torch.empty((M, W.rows), dtype=torch.bfloat16, device=x.device)
+    out = out if out is not None else torch.empty(M, W.rows, dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = fused_workspace(fmt, M, K, x.device)
     ws_bytes = workspace.numel() * workspace.element_size()
@@ -426,8 +426,8 @@ def _need(ok, what: str) -> None:
 
 
 def _rows_ok(x: torch.Tensor, what: str) -> None:
-    _need(x.dtype == torch.bfloat16 and x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] <= 1),
-          f"{what}: a bf16 matrix with contiguous rows is wanted")
+    if not (x.dtype == torch.bfloat16 and x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] <= 1)):
+        raise ValueError(f"{what}: a bf16 matrix with contiguous rows is wanted")
 
 
 def _pitch(x: torch.Tensor) -> int:
@@ -461,7 +461,7 @@ def route(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = None
     _same_device(ids, workspace)
     offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
     row_token = torch.empty(n, dtype=torch.int32, device=dev)
-    slot = torch.empty((tokens, choices), dtype=torch.int32, device=dev)
+    slot = torch.empty(tokens, choices, dtype=torch.int32, device=dev)
     need = mx_route_workspace_bytes(tokens, choices, experts)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -548,7 +548,7 @@ def gemm_grouped(A: MxTensor, B: MxTensor, offsets: torch.Tensor, out: torch.Ten
           _nbytes(B.scales) >= E * mx_scales_bytes(B.fmt, B.rows, B.cols) and
           (B.gscale is None or B.gscale.numel() >= E), "B: fewer matrices than groups")
     if out is None:
-        out = torch.empty((A.rows, B.rows), dtype=torch.bfloat16, device=A.codes.device)
+        out = torch.empty(A.rows, B.rows, dtype=torch.bfloat16, device=A.codes.device)
     else:
         _rows_ok(out, "out")
         _need(out.shape == (A.rows, B.rows), "out: another size")
@@ -571,7 +571,7 @@ def combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor, out: tor
     tokens, choices = slot.shape
     rows, cols = y.shape
     if out is None:
-        out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=y.device)
+        out = torch.empty(tokens, cols, dtype=torch.bfloat16, device=y.device)
     else:
         _rows_ok(out, "out")
         _need(out.shape == (tokens, cols), "out: another size")

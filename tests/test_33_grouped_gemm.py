@@ -324,3 +324,26 @@ def test_rows_to_several_places_in_two_graphs_at_once():
     for _, _, got, want, *_ in cases:
         for t in got:
             assert torch.equal(t.codes, want.codes) and torch.equal(t.scales, want.scales)
+
+
+@pytest.mark.parametrize("fmt", [6, 0, 3])
+def test_rows_to_several_places_with_overlapping_offsets(fmt):
+    """Offsets that descend enter rows twice: nothing is written outside the buffers, and both ways agree."""
+    tokens, T, K = 400, 2000, 1536
+    od = torch.tensor([-5, 1600, 800, 10 ** 6], dtype=torch.int32, device="cuda")   # [0, 1600), none, [800, 2000)
+    x, idx, g = activations(1, tokens, K), scattered(2, tokens, T, "random"), gs(fmt)
+    assert mx.mx_quantize_grouped_workspace_bytes(T, tokens, K) > 0
+    codes, scales = mx.mx_codes_bytes(fmt, T, K), mx.mx_grouped_scales_bytes(fmt, T, 3, K)
+    got = []
+    for ws in (True, False):
+        c, s = (torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda") for n in (codes, scales))
+        out = mx.MxTensor(fmt, T, K, c, s, None if g is None else torch.empty(1, device="cuda"))
+        if ws:
+            mx.quantize_grouped(x, od, fmt, row_index=idx, gscale=g, out=out)
+        else:
+            mx.check(mx.mx_quantize_grouped(fmt, x.data_ptr(), tokens, K, K, idx.data_ptr(), mx.MxGroupsC(3, 0, od.data_ptr()),
+                                            out.c(), None if g is None else g.data_ptr(), None, 0, mx._stream()))
+        torch.cuda.synchronize()
+        assert (c[codes:] == 0x5A).all() and (s[scales:] == 0x5A).all()
+        got.append((c, s))
+    assert torch.equal(got[0][0], got[1][0])
